@@ -44,6 +44,16 @@ class sdv2_motion_config(ctypes.Structure):
                 ("s_min", c_double), ("s_max", c_double), ("s_init", c_double)]
 
 
+DT_BF16, DT_FP16 = 0, 1
+DTYPES = {"bf16": DT_BF16, "fp16": DT_FP16}
+
+
+class sdv2_prompt_config(ctypes.Structure):
+    _fields_ = [("heads", c_int32), ("kv_heads", c_int32), ("head_dim", c_int32), ("block_tokens", c_int32),
+                ("dtype", c_int32), ("tokens", c_int64), ("q_stride", c_int64), ("k_stride", c_int64),
+                ("v_stride", c_int64), ("out_stride", c_int64)]
+
+
 class SDV2Error(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {message}")
@@ -82,6 +92,9 @@ _SIGNATURES = [
                                       POINTER(c_int32)]),
     ("sdv2_attention_pair_mode", c_int32, [POINTER(sdv2_cache_config), POINTER(c_int64), c_int32]),
     ("sdv2_append_attention_mode", c_int32, [POINTER(sdv2_cache_config), POINTER(c_int64), c_int32]),
+    ("sdv2_prompt_attention", c_int32, [POINTER(sdv2_prompt_config), c_void_p, c_void_p, c_void_p, c_void_p,
+                                        POINTER(c_int64), c_int32, c_float, c_void_p]),
+    ("sdv2_prompt_check", c_int32, []),
     ("sdv2_launch_count", c_uint64, []),
     ("sdv2_last_error", c_char_p, []),
     ("sdv2_version", c_char_p, []),
@@ -305,6 +318,19 @@ def sdv2_attention_plan(cfg: sdv2_cache_config, keys, sm_count: int):
     _check(lib().sdv2_attention_plan(ctypes.byref(cfg), arr, sm_count, ctypes.byref(whole), ctypes.byref(pieces)),
            "sdv2_attention_plan")
     return int(whole.value), int(pieces.value)
+
+
+def sdv2_prompt_attention(cfg: sdv2_prompt_config, q, k, v, out, offsets, softmax_scale: float, stream=None) -> None:
+    """q, k, v, out: device pointers (or contiguous device tensors); offsets: n_seqs + 1 host integers."""
+    n = len(offsets)
+    if n < 1:
+        raise ValueError("offsets needs at least one entry")
+    _check(lib().sdv2_prompt_attention(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(out), (c_int64 * n)(*offsets),
+                                       n - 1, float(softmax_scale), _stream(stream)), "sdv2_prompt_attention")
+
+
+def sdv2_prompt_check() -> int:
+    return int(lib().sdv2_prompt_check())
 
 
 def sdv2_launch_count() -> int:

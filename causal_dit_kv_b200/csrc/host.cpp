@@ -20,8 +20,7 @@
 
 #include <cudaTypedefs.h>
 
-#include "sdv2.h"
-#include "sdv2_internal.h"
+#include "host_common.h"
 
 using namespace sdv2;
 
@@ -29,6 +28,10 @@ namespace {
 
 thread_local std::string g_err;
 std::atomic<uint64_t> g_launches{0};
+
+}  // namespace
+
+namespace sdv2 {
 
 sdv2_status fail(sdv2_status st, const char *fmt, ...) {
     char buf[512];
@@ -44,8 +47,31 @@ sdv2_status cuda_fail(cudaError_t e, const char *what) {
     return fail(SDV2_E_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-inline uint64_t align_up(uint64_t x, uint64_t a) { return (x + a - 1) / a * a; }
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+void count_launch() { g_launches.fetch_add(1); }
+
+PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    }
+    return fn;
+}
+
+sdv2_status check_device(int device) {
+    int cur = -1;
+    cudaError_t e = cudaGetDevice(&cur);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (cur != device) return fail(SDV2_E_ARG, "current device %d is not the handle's device %d", cur, device);
+    return SDV2_OK;
+}
+
+}  // namespace sdv2
+
+namespace {
 
 int32_t slot_of(int64_t f, int32_t S, int32_t W) {
     if (f < 0) return -1;
@@ -278,18 +304,6 @@ int64_t max_kv_tiles(const Geometry &g, const int64_t *keys, int n) {
     return m;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q{};
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-    }
-    return fn;
-}
-
 }  // namespace
 
 struct sdv2_cache {
@@ -316,14 +330,6 @@ struct sdv2_motion {
 };
 
 namespace {
-
-sdv2_status check_device(int device) {
-    int cur = -1;
-    cudaError_t e = cudaGetDevice(&cur);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (cur != device) return fail(SDV2_E_ARG, "current device %d is not the handle's device %d", cur, device);
-    return SDV2_OK;
-}
 
 sdv2_status check_stream_frames(const sdv2_cache *c, int32_t layer, const int64_t *f0, bool after_append,
                                 int *active_out) {

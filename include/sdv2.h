@@ -379,6 +379,49 @@ int32_t sdv2_attention_pair_mode(const sdv2_cache_config *cfg, const int64_t *ke
 int32_t sdv2_append_attention_mode(const sdv2_cache_config *cfg, const int64_t *chunk_first_frame,
                                    int32_t sm_count);
 
+/* ------------------------------------------------------------------------
+ * Prompt attention: the first pass over whole packed prompts or clips.
+ * ---------------------------------------------------------------------- */
+
+/* 16-bit element types of the prompt attention and of the paged cache. */
+enum { SDV2_DT_BF16 = 0, SDV2_DT_FP16 = 1 };
+
+typedef struct {
+    int32_t heads;          /* Hq: query heads, a multiple of kv_heads, at most 1024 */
+    int32_t kv_heads;       /* Hkv: query head h reads key head h / (Hq / Hkv) */
+    int32_t head_dim;       /* d: 64 or 128 */
+    int32_t block_tokens;   /* b >= 1: causal by blocks of b tokens (1: token by token) */
+    int32_t dtype;          /* SDV2_DT_BF16 or SDV2_DT_FP16, of q, k, v and out */
+    int64_t tokens;         /* T: rows of q, k, v and out (< 2^30) */
+    /* elements between consecutive tokens, multiples of 8; 0: contiguous.  A token's heads
+     * are contiguous, so q, k and v may be slices of one fused projection's output. */
+    int64_t q_stride, k_stride, v_stride, out_stride;
+} sdv2_prompt_config;
+
+/* Causal attention within each of n_seqs packed sequences:
+ *   out_i = sum_j softmax_j(softmax_scale * q_i . k_j) v_j
+ * over the keys j of i's own sequence with floor(j / b) <= floor(i / b), places counted
+ * from the sequence's start (b = T'*N of a cache config is the chunk-causal mask of
+ * sdv2_chunk_attention; a b of at least the longest sequence masks nothing).  Queries and
+ * keys are taken as given (RoPE, if any, applied by the caller).
+ * q: device [T][Hq][d]; k, v: device [T][Hkv][d]; out: device [T][Hq][d], overlapping none
+ *   of them.
+ * offsets: HOST int64 [n_seqs + 1], not decreasing, in 0..T: sequence s is rows
+ *   offsets[s] .. offsets[s+1] - 1.  Empty sequences are allowed; rows of out outside every
+ *   sequence stay as they were.
+ * Scores, softmax and sums are fp32; the probabilities are rounded to 16 bits before the
+ * second product.  What lies outside a sequence, NaN and infinities included, has no part
+ * in it; a value that is not finite inside a sequence may reach any row of that sequence.
+ * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN, SDV2_E_CUDA; SDV2_E_STATE without host
+ * memory. */
+sdv2_status sdv2_prompt_attention(const sdv2_prompt_config *cfg, const void *q, const void *k, const void *v,
+                                  void *out, const int64_t *offsets, int32_t n_seqs, float softmax_scale,
+                                  sdv2_stream stream);
+
+/* Synchronise the current device and report waits of its prompt kernels that ran past
+ * their bound (SDV2_E_DEVICE; the record is cleared). */
+sdv2_status sdv2_prompt_check(void);
+
 /* Kernels launched by this library in this process so far. */
 uint64_t sdv2_launch_count(void);
 /* Thread-local message describing the last failing call ("" if none). */
