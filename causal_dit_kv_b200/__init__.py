@@ -6,5 +6,6 @@ wraps a cache and a motion state with torch-owned device buffers.
 """
 from . import binding  # noqa: F401
 from .binding import SDV2Error  # noqa: F401
+from .pages import PagedKVCache  # noqa: F401
 from .prompt import prompt_attention, prompt_check  # noqa: F401
 from .stream import KVCache, MotionState  # noqa: F401

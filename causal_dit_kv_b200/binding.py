@@ -54,6 +54,17 @@ class sdv2_prompt_config(ctypes.Structure):
                 ("v_stride", c_int64), ("out_stride", c_int64)]
 
 
+class sdv2_pages_config(ctypes.Structure):
+    _fields_ = [(name, c_int32) for name in ("streams", "layers", "heads", "kv_heads", "head_dim", "page_tokens", "pages",
+                                             "stream_pages", "max_queries", "block_tokens", "dtype")]
+
+
+class sdv2_pages_layout(ctypes.Structure):
+    _fields_ = [(name, c_uint64) for name in ("k_offset", "v_offset", "layer_stride", "table_offset", "length_offset",
+                                              "version_offset", "status_offset", "scratch_offset", "scratch_bytes",
+                                              "total_bytes")]
+
+
 class SDV2Error(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         super().__init__(f"{where}: {STATUS_NAMES.get(status, status)}: {message}")
@@ -95,6 +106,22 @@ _SIGNATURES = [
     ("sdv2_prompt_attention", c_int32, [POINTER(sdv2_prompt_config), c_void_p, c_void_p, c_void_p, c_void_p,
                                         POINTER(c_int64), c_int32, c_float, c_void_p]),
     ("sdv2_prompt_check", c_int32, []),
+    ("sdv2_pages_bytes", c_size_t, [POINTER(sdv2_pages_config)]),
+    ("sdv2_pages_layout_of", c_int32, [POINTER(sdv2_pages_config), POINTER(sdv2_pages_layout)]),
+    ("sdv2_pages_create", c_int32, [POINTER(sdv2_pages_config), c_void_p, c_size_t, POINTER(c_void_p)]),
+    ("sdv2_pages_destroy", c_int32, [c_void_p]),
+    ("sdv2_pages_extend", c_int32, [c_void_p, POINTER(c_int32), c_void_p]),
+    ("sdv2_pages_write", c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, POINTER(c_int32), c_void_p]),
+    ("sdv2_pages_attention", c_int32,
+     [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, POINTER(c_int32), c_float, c_void_p]),
+    ("sdv2_pages_fork", c_int32, [c_void_p, c_int32, POINTER(c_int32), c_int32, c_int32, c_void_p]),
+    ("sdv2_pages_free", c_int32, [c_void_p, POINTER(c_int32), c_int32, c_void_p]),
+    ("sdv2_pages_compact", c_int32, [c_void_p, POINTER(c_int32), c_void_p]),
+    ("sdv2_pages_query", c_int32,
+     [c_void_p, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, POINTER(c_int32), POINTER(c_int32)]),
+    ("sdv2_pages_used", c_int32, [c_void_p]),
+    ("sdv2_pages_layout_get", c_int32, [c_void_p, POINTER(sdv2_pages_layout)]),
+    ("sdv2_pages_check", c_int32, [c_void_p]),
     ("sdv2_launch_count", c_uint64, []),
     ("sdv2_last_error", c_char_p, []),
     ("sdv2_version", c_char_p, []),
@@ -331,6 +358,104 @@ def sdv2_prompt_attention(cfg: sdv2_prompt_config, q, k, v, out, offsets, softma
 
 def sdv2_prompt_check() -> int:
     return int(lib().sdv2_prompt_check())
+
+
+def make_pages_config(streams, layers, heads, kv_heads, head_dim, pages, page_tokens=64, stream_pages=None,
+                      max_queries=None, block_tokens=1, dtype="bf16") -> sdv2_pages_config:
+    """stream_pages None: as many as the pool has; max_queries None: one for every stream."""
+    cfg = sdv2_pages_config()
+    cfg.streams, cfg.layers, cfg.heads, cfg.kv_heads, cfg.head_dim = streams, layers, heads, kv_heads, head_dim
+    cfg.page_tokens, cfg.pages = page_tokens, pages
+    cfg.stream_pages = pages if stream_pages is None else stream_pages
+    cfg.max_queries = streams if max_queries is None else max_queries
+    cfg.block_tokens = min(block_tokens, (1 << 31) - 1)
+    cfg.dtype = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    return cfg
+
+
+def int32_array(values):
+    """A ctypes int32 array of host integers."""
+    if isinstance(values, ctypes.Array):
+        return values
+    return (c_int32 * len(values))(*values)
+
+
+def sdv2_pages_bytes(cfg: sdv2_pages_config) -> int:
+    n = lib().sdv2_pages_bytes(ctypes.byref(cfg))
+    if n == 0:
+        raise SDV2Error(SDV2_E_SHAPE, "sdv2_pages_bytes", lib().sdv2_last_error().decode())
+    return int(n)
+
+
+def sdv2_pages_layout_of(cfg: sdv2_pages_config) -> sdv2_pages_layout:
+    out = sdv2_pages_layout()
+    _check(lib().sdv2_pages_layout_of(ctypes.byref(cfg), ctypes.byref(out)), "sdv2_pages_layout_of")
+    return out
+
+
+def sdv2_pages_create(cfg: sdv2_pages_config, dev_buf, nbytes: int) -> int:
+    h = c_void_p()
+    _check(lib().sdv2_pages_create(ctypes.byref(cfg), _ptr(dev_buf), nbytes, ctypes.byref(h)), "sdv2_pages_create")
+    return h.value
+
+
+def sdv2_pages_destroy(pages: int) -> None:
+    _check(lib().sdv2_pages_destroy(pages), "sdv2_pages_destroy")
+
+
+def sdv2_pages_extend(pages: int, counts, stream=None) -> None:
+    """counts: one host integer per stream (as for every call with counts)."""
+    _check(lib().sdv2_pages_extend(pages, int32_array(counts), _stream(stream)), "sdv2_pages_extend")
+
+
+def sdv2_pages_write(pages: int, layer: int, k, v, k_stride: int, v_stride: int, counts, stream=None) -> None:
+    _check(lib().sdv2_pages_write(pages, layer, _ptr(k), _ptr(v), k_stride, v_stride, int32_array(counts),
+                                  _stream(stream)), "sdv2_pages_write")
+
+
+def sdv2_pages_attention(pages: int, layer: int, q, out, q_stride: int, out_stride: int, counts, softmax_scale: float,
+                         stream=None) -> None:
+    _check(lib().sdv2_pages_attention(pages, layer, _ptr(q), _ptr(out), q_stride, out_stride, int32_array(counts),
+                                      float(softmax_scale), _stream(stream)), "sdv2_pages_attention")
+
+
+def sdv2_pages_fork(pages: int, src: int, dst, deep: bool = False, stream=None) -> None:
+    _check(lib().sdv2_pages_fork(pages, src, int32_array(dst), len(dst), 1 if deep else 0, _stream(stream)),
+           "sdv2_pages_fork")
+
+
+def sdv2_pages_free(pages: int, streams, stream=None) -> None:
+    _check(lib().sdv2_pages_free(pages, int32_array(streams), len(streams), _stream(stream)), "sdv2_pages_free")
+
+
+def sdv2_pages_compact(pages: int, stream=None) -> int:
+    used = c_int32()
+    _check(lib().sdv2_pages_compact(pages, ctypes.byref(used), _stream(stream)), "sdv2_pages_compact")
+    return int(used.value)
+
+
+def sdv2_pages_query(pages: int, stream_index: int):
+    """(tokens, list of page ids, leading pages shared by the stream's whole group)."""
+    tokens, n, shared = c_int32(), c_int32(), c_int32()
+    _check(lib().sdv2_pages_query(pages, stream_index, ctypes.byref(tokens), None, 0, ctypes.byref(n),
+                                  ctypes.byref(shared)), "sdv2_pages_query")
+    ids = (c_int32 * max(n.value, 1))()
+    _check(lib().sdv2_pages_query(pages, stream_index, None, ids, n.value, None, None), "sdv2_pages_query")
+    return int(tokens.value), list(ids)[:n.value], int(shared.value)
+
+
+def sdv2_pages_used(pages: int) -> int:
+    return int(lib().sdv2_pages_used(pages))
+
+
+def sdv2_pages_layout_get(pages: int) -> sdv2_pages_layout:
+    out = sdv2_pages_layout()
+    _check(lib().sdv2_pages_layout_get(pages, ctypes.byref(out)), "sdv2_pages_layout_get")
+    return out
+
+
+def sdv2_pages_check(pages: int) -> int:
+    return int(lib().sdv2_pages_check(pages))
 
 
 def sdv2_launch_count() -> int:

@@ -1,0 +1,593 @@
+// Attention of every stream's newest tokens over the pages of its keys, on the sm_100a
+// tensor cores; streams that share leading pages have those read once for all of them.
+//
+// The softmax over a stream's keys splits into the keys of the group's common pages and the
+// stream's own: each part gives an unnormalised output, a row maximum and a row sum, which
+// merge as in the online softmax.  The common part's query tile holds the rows of all the
+// group's streams, so its keys are read once per 128 rows.
+//
+// Few rows and many keys: the bound is HBM, so the work is cut evenly by keys.  All units
+// (128-row tile, key head) are laid end to end in KV tiles of 128 keys and every CTA, one per
+// SM, takes an equal run of tiles, crossing units as it goes; a unit cut by a border leaves
+// one partial result per CTA.  Rings of K and V tiles (192 KB at d = 128) keep loads in flight
+// across units.
+//   warp 0      looks up pages, one TMA box per page and 64 channels (a lane each)
+//   warp 1      MMA issuer: tile i of a run goes to accumulator set i & 1
+//   warp 2      zeroes the rows of a run's last V tile behind its keys
+//   warps 4..7  softmax of set 0, 8..11 of set 1 (thread = query row); both gather the
+//               queries into shared memory and merge the two sets at the end
+// A query tile holds the rows (token, head of the group); rows beyond them cost no
+// exponentials.
+#include <atomic>
+
+#include "attn_core.cuh"
+#include "token_ops.h"
+
+namespace sdv2 {
+
+template <int D>
+struct PagesLayout {
+    static constexpr int kTile = 128 * D * 2;
+    static constexpr int kSub = 128 * 128;
+    static constexpr int kStages = D == 128 ? 3 : 6;      // of K and of V
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + kTile;
+    static constexpr int kV = kK + kStages * kTile;
+    static constexpr int kXm = kQ;                        // (max, sum) of both sets, once the queries are done with
+    static constexpr int kBar = kV + kStages * kTile;
+    static constexpr int kQReady = 0;
+    static constexpr int kKFull = 1, kKEmpty = kKFull + kStages;
+    static constexpr int kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages;
+    static constexpr int kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 2;
+    static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1, kNumBars = kDrain + 1;
+    static constexpr int kMisc = kBar + kNumBars * 8;
+    static constexpr int kAlloc = kMisc + 16 + 1024;
+    static_assert(kAlloc <= 232448, "shared memory of one CTA");
+};
+
+// A CTA's run of tiles within one unit.
+struct PagesRun {
+    int sec, row_tile, head;     // section, 128-row tile, key head
+    int n_rows;                  // query rows of the tile
+    int begin, n;                // first KV tile of the run in the unit, tiles (0: nothing to read)
+    int keys;                    // keys of the unit's page range (they end inside its last tile)
+    int base;                    // place in the stream of its first key
+    int len;                     // tokens of the stream
+    int piece;                   // which piece of the unit this is (0: its first)
+    bool whole, common;          // the unit's only piece; keys of common pages
+};
+
+template <int kS, int kM>
+__device__ __forceinline__ PagesRun pages_run(const PagesAttnParams<kS, kM> &p, int pos, int end, int *taken) {
+    int lo = 0, hi = p.n_sections;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.section[mid].start <= pos)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const PageSection &s = p.section[lo];
+    PagesRun r;
+    r.sec = lo;
+    const int unit = (pos - s.start) / s.tiles;
+    r.begin = pos - s.start - unit * s.tiles;
+    *taken = min(s.tiles - r.begin, end - pos);
+    r.row_tile = unit / p.v.kv_heads;
+    r.head = unit - r.row_tile * p.v.kv_heads;
+    r.common = s.keys >= 0;
+    r.base = s.page0 << p.v.page_log2;
+    r.len = p.v.lengths[s.stream];
+    const int tokens = min(p.tile_tokens, s.n_tokens - r.row_tile * p.tile_tokens);
+    r.n_rows = tokens * p.group;
+    r.keys = r.common ? s.keys : r.len - r.base;
+    // KV tiles that the tile's rows see: all of the common keys, or up to its last token's
+    int tiles = (r.keys + 127) >> 7;
+    if (!r.common) {
+        const int last = r.len - s.n_tokens + r.row_tile * p.tile_tokens + tokens - 1;
+        tiles = (min(r.len, (last / p.block + 1) * p.block) - r.base + 127) >> 7;
+    }
+    // (the unit's last piece takes what a longer stream has grown since the work was cut)
+    const bool last_piece = r.begin + *taken == s.tiles;
+    r.n = max(0, (last_piece ? tiles : min(tiles, r.begin + *taken)) - r.begin);
+    const int64_t first = static_cast<int64_t>(s.start) + static_cast<int64_t>(unit) * s.tiles;
+    r.piece = static_cast<int>(blockIdx.x - ((first + 1) * p.n_ctas - 1) / p.n_tiles);
+    r.whole = r.begin == 0 && last_piece;
+    return r;
+}
+
+// Valid keys of the run's last tile if the range ends inside it (0: it does not).
+__device__ __forceinline__ int tail_keys(const PagesRun &r) {
+    const int left = r.keys - (r.begin + r.n - 1) * 128;
+    return r.n > 0 && left < 128 ? left : 0;
+}
+
+// Packed token of the `place`-th query token of a section.
+template <int kS, int kM>
+__device__ __forceinline__ int query_token(const PagesAttnParams<kS, kM> &p, const PageSection &s, int place) {
+    if (s.keys < 0) return s.token0 + place;
+    const int x = s.token0 + place;
+    int lo = 0, hi = p.n_members;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.member_first[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return p.member_token[lo] + x - p.member_first[lo];
+}
+
+template <int D, bool HALF, int kS, int kM>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    pages_attention_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p, const __grid_constant__ CUtensorMap tmap_k,
+                           const __grid_constant__ CUtensorMap tmap_v) {
+    using L = PagesLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBar);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
+    volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + L::kMisc + 4);
+    uint32_t *status = p.v.status;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < L::kNumBars; ++b)
+            mbar_init(&bars[b], b == L::kQReady ? 256 : (b == L::kPFull || b == L::kPFull + 1 ? 128 : 1));
+        *abort_flag = 0u;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmap_k);
+        tma_prefetch_desc(&tmap_v);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependency_wait();                     // queries, pages and tables may come from the kernels before
+    grid_launch_dependents();
+
+    // this CTA's tiles (none if the tables are not those of the call)
+    int pos0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.n_tiles / p.n_ctas);
+    int end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.n_tiles / p.n_ctas);
+    if (*p.v.version != p.v.expect) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kStatusStale);
+        end = pos0 = 0;
+    }
+    const int page_log2 = p.v.page_log2;
+
+    if (warp < 4) {
+        regs_dec<80>();
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer (the whole warp)
+            const int ppt_log2 = 7 - page_log2, ppt = 1 << ppt_log2;   // pages of a KV tile
+            const int box = lane / (D / 64), kb = lane % (D / 64);     // this lane's page of the tile, 64 channels
+            const uint32_t box_bytes = 128u << page_log2;
+            int kc = 0, vc = 0;
+            bool ok = true;
+            for (int pos = pos0, taken; ok && pos < end; pos += taken) {
+                const PagesRun r = pages_run(p, pos, end, &taken);
+                if (r.n == 0) continue;
+                const PageSection &s = p.section[r.sec];
+                const int32_t *row = p.v.table + static_cast<int64_t>(s.stream) * p.v.width + s.page0;
+                const int n_pages = (r.keys + (1 << page_log2) - 1) >> page_log2;   // of the key range
+                // page ids of the run, 32 at a time, the next 32 in flight
+                int batch = r.begin << ppt_log2;                     // index of ids_now's first page
+                const int last_page = n_pages - 1;
+                int ids_now = row[min(batch + lane, last_page)];
+                int ids_next = row[min(batch + 32 + lane, last_page)];
+                int id_k[3];                                          // this lane's page of K tiles it + 2, it + 1, it
+                auto page_of = [&](int tile) {                        // (tiles in order)
+                    const int first = (r.begin + tile) << ppt_log2;
+                    if (first - batch >= 32) {
+                        batch += 32;
+                        ids_now = ids_next;
+                        ids_next = row[min(batch + 32 + lane, last_page)];
+                    }
+                    return __shfl_sync(0xffffffffu, ids_now, first - batch + min(box, ppt - 1));
+                };
+                auto load = [&](int tile, int id, const CUtensorMap *map, int base, int full, int empty, int &c) {
+                    const int st = c % L::kStages;
+                    if (!warp_wait_all(&bars[empty + st], ((c / L::kStages) & 1) ^ 1, abort_flag, status, kStatusTmaWait))
+                        return false;
+                    const int first = (r.begin + tile) << ppt_log2;
+                    const int boxes = min(ppt, n_pages - first);      // pages that there are
+                    if (lane == 0) mbar_arrive_expect_tx(&bars[full + st], boxes * (D / 64) * box_bytes);
+                    __syncwarp();
+                    if (box < boxes)
+                        tma_load_3d(smem + base + st * L::kTile + kb * L::kSub + box * box_bytes, map, &bars[full + st],
+                                    kb * 64, 0, id * p.v.kv_heads + r.head);
+                    ++c;
+                    return true;
+                };
+                // K runs two tiles ahead of V: scores of both sets come before the first product with V
+                id_k[2] = page_of(0);
+                ok = load(0, id_k[2], &tmap_k, L::kK, L::kKFull, L::kKEmpty, kc);
+                id_k[1] = id_k[2];
+                if (ok && r.n > 1) {
+                    id_k[1] = page_of(1);
+                    ok = load(1, id_k[1], &tmap_k, L::kK, L::kKFull, L::kKEmpty, kc);
+                }
+                for (int it = 0; ok && it < r.n; ++it) {
+                    ok = load(it, id_k[2], &tmap_v, L::kV, L::kVFull, L::kVEmpty, vc);
+                    id_k[0] = 0;
+                    if (ok && it + 2 < r.n) {
+                        id_k[0] = page_of(it + 2);
+                        ok = load(it + 2, id_k[0], &tmap_k, L::kK, L::kKFull, L::kKEmpty, kc);
+                    }
+                    id_k[2] = id_k[1];
+                    id_k[1] = id_k[0];
+                }
+            }
+            if (!ok && lane == 0) {             // let every copy in flight land before the CTA leaves
+                const uint64_t t0 = global_timer_ns();
+                auto drain = [&](int c, int full) {
+                    for (int i = max(0, c - L::kStages); i < c; ++i)
+                        while (!mbar_try_wait(&bars[full + i % L::kStages], (i / L::kStages) & 1))
+                            if (global_timer_ns() - t0 > kWaitLimitNs) break;
+                };
+                drain(kc, L::kKFull);
+                drain(vc, L::kVFull);
+            }
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc_qk = idesc_16_f32<HALF>(128, 128, 0, 0);
+            constexpr uint32_t idesc_pv = idesc_16_f32<HALF>(128, D, 0, 1);
+            const uint64_t dq = smem_desc_sw128(smem_addr(smem + L::kQ), 16, 1024);
+            const uint64_t dk = smem_desc_sw128(smem_addr(smem + L::kK), 16, 1024);
+            const uint64_t dv = smem_desc_sw128(smem_addr(smem + L::kV), L::kSub, 1024);
+            int kc = 0, vc = 0, runs = 0, fixes = 0, pc[2] = {0, 0};
+            bool ok = true;
+            auto issue_qk = [&](int t) {        // the next K tile's scores into set t
+                const int st = kc % L::kStages;
+                if (!mbar_wait(&bars[L::kKFull + st], (kc / L::kStages) & 1, abort_flag, status, kStatusMmaWait))
+                    return false;
+                tc_fence_after();
+                const uint64_t b0 = dk + static_cast<uint64_t>(st * (L::kTile >> 4));
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = static_cast<uint64_t>(((kk >> 2) * L::kSub + (kk & 3) * 32) >> 4);
+                    umma_ss(tmem + t * 128, dq + off, b0 + off, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&bars[L::kSFull + t]);
+                umma_commit(&bars[L::kKEmpty + st]);
+                ++kc;
+                return true;
+            };
+            for (int pos = pos0, taken; ok && pos < end; pos += taken) {
+                const PagesRun r = pages_run(p, pos, end, &taken);
+                if (r.n == 0) continue;
+                ok = mbar_wait(&bars[L::kQReady], runs & 1, abort_flag, status, kStatusMmaWait);
+                ++runs;
+                if (!ok) break;
+                tc_fence_after();
+                ok = issue_qk(0) && (r.n < 2 || issue_qk(1));
+                const bool tail = tail_keys(r) > 0;
+                for (int it = 0; ok && it < r.n; ++it) {
+                    const int t = it & 1, st = vc % L::kStages;
+                    ok = mbar_wait(&bars[L::kVFull + st], (vc / L::kStages) & 1, abort_flag, status, kStatusMmaWait);
+                    if (ok && tail && it == r.n - 1) {
+                        mbar_arrive(&bars[L::kVAsk]);
+                        ok = mbar_wait(&bars[L::kVFix], fixes & 1, abort_flag, status, kStatusMmaWait);
+                        ++fixes;
+                    }
+                    if (ok) ok = mbar_wait(&bars[L::kPFull + t], (t ? pc[1] : pc[0]) & 1, abort_flag, status, kStatusMmaWait);
+                    ++(t ? pc[1] : pc[0]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t b0 = dv + static_cast<uint64_t>(st * (L::kTile >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_ts(tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                                b0 + static_cast<uint64_t>((kk * 2048) >> 4), idesc_pv, (it >= 2 || kk > 0) ? 1u : 0u);
+                    umma_commit(&bars[L::kVEmpty + st]);
+                    ++vc;
+                    if (it + 2 < r.n)
+                        ok = issue_qk(t);
+                    else
+                        umma_commit(&bars[L::kOFull + t]);
+                }
+            }
+            // every MMA issued so far has finished before TMEM is released
+            umma_commit(&bars[L::kDrain]);
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(&bars[L::kDrain], 0)) {
+                if (global_timer_ns() - t0 > kWaitLimitNs) {
+                    atomicOr(status, kStatusMmaWait);
+                    break;
+                }
+            }
+        } else if (warp == 2) {
+            // ------------------------------------------------ ends of key ranges in V
+            int vc = 0, fixes = 0;
+            for (int pos = pos0, taken; pos < end; pos += taken) {
+                const PagesRun r = pages_run(p, pos, end, &taken);
+                vc += r.n;
+                const int valid = tail_keys(r);
+                if (valid == 0) continue;
+                if (!warp_wait_all(&bars[L::kVAsk], fixes & 1, abort_flag, status, kStatusTmaWait)) break;
+                ++fixes;
+                zero_tail_rows<D>(smem + L::kV + (vc - 1) % L::kStages * L::kTile, valid, lane);
+                if (lane == 0) mbar_arrive(&bars[L::kVFix]);
+            }
+        }
+    } else {
+        // ------------------------------------------------ queries, softmax and epilogue
+        regs_inc<208>();
+        const int t = (warp - 4) >> 2;               // accumulator set
+        const int row = ((warp & 3) << 5) + lane;    // query row (TMEM lane)
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) << 5) << 16;
+        const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
+        float2 *xm = reinterpret_cast<float2 *>(smem + L::kXm);
+        int sc = 0, oc[2] = {0, 0};
+        bool ok = true;
+        for (int pos = pos0, taken; ok && pos < end; pos += taken) {
+            const PagesRun r = pages_run(p, pos, end, &taken);
+            const PageSection &s = p.section[r.sec];
+            const bool valid = row < r.n_rows;
+            const bool busy = ((warp & 3) << 5) < r.n_rows;        // the warp has rows
+            const int place = r.row_tile * p.tile_tokens + (valid ? row / p.group : 0);
+            const int head = r.head * p.group + row % p.group;
+            const int token = query_token(p, s, place);
+            if (r.n > 0) {
+                // the row's queries, half of its channels per set, to their 128-byte-swizzled places
+                // (every score of the run before has been read: its products with Q are done)
+                constexpr int kC = D / 16;                           // 16-byte chunks of half a row
+                uint4 x[kC];
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(token) * p.q_stride +
+                                                                   head * D) + t * kC;
+#pragma unroll
+                for (int c = 0; c < kC; ++c) x[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < kC; ++c) {
+                    const int cc = t * kC + c;                       // chunk of the whole row
+                    *reinterpret_cast<uint4 *>(smem + L::kQ + (cc >> 3) * L::kSub + row * 128 + (((cc & 7) ^ (row & 7)) << 4)) = x[c];
+                }
+                fence_proxy_async_shared();
+                tc_fence_before();
+                mbar_arrive(&bars[L::kQReady]);
+            }
+            // keys the row sees, from the range's first
+            int seen = r.keys;
+            if (!r.common) {
+                const int at = r.len - s.n_tokens + place;
+                seen = min(r.len, (at / p.block + 1) * p.block) - r.base;
+            }
+            const int n_mine = (r.n + 1 - t) >> 1;
+            float m_run = -INFINITY, l_run = 0.0f;
+            for (int it = 0; it < n_mine; ++it, ++sc) {
+                ok = warp_wait_all(&bars[L::kSFull + t], sc & 1, abort_flag, status, kStatusSoftmaxWait);
+                if (!ok) break;
+                if (busy) {
+                    tc_fence_after();
+                    ScoreRow x;
+                    load_scores(s_tmem, x);
+                    const int cols = seen - (r.begin + 2 * it + t) * 128;
+                    if (__any_sync(0xffffffffu, cols < 128)) mask_scores(x, cols);
+                    const float m_tile = max_score(x) * p.scale_log2;
+                    bool rescale = false;
+                    float alpha = 1.0f;
+                    // (a row may see none of a tile's keys: its maximum stays -inf, its P is 0)
+                    if (m_tile > m_run + kCoreRescale || m_run == -INFINITY) {
+                        rescale = it > 0;
+                        alpha = m_run == -INFINITY ? 0.0f : ex2_approx(m_run - m_tile);
+                        l_run *= alpha;
+                        m_run = m_tile;
+                    }
+                    l_run += exp_store<HALF>(x, p.scale_log2, m_run == -INFINITY ? 0.0f : -m_run, s_tmem);
+                    if (__any_sync(0xffffffffu, rescale)) rescale_row<D>(o_tmem, alpha);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                mbar_arrive(&bars[L::kPFull + t]);
+            }
+
+            // ---- both sets merged: thread (t, row) takes columns [t D / 2, (t + 1) D / 2)
+            // (a warp whose wait ran out comes to the barrier too: all 256 threads leave together)
+            const bool has0 = r.n > 0, has1 = r.n > 1;
+            if (ok && has0) ok = warp_wait_all(&bars[L::kOFull + 0], oc[0]++ & 1, abort_flag, status, kStatusSoftmaxWait);
+            if (ok && has1) ok = warp_wait_all(&bars[L::kOFull + 1], oc[1]++ & 1, abort_flag, status, kStatusSoftmaxWait);
+            xm[t * 128 + row] = make_float2(m_run, l_run);
+            ok = named_bar_and(1, 256, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const float2 a0 = xm[row], a1 = xm[128 + row];
+            const float m = fmaxf(a0.x, a1.x);
+            const float w0 = a0.x == -INFINITY ? 0.0f : ex2_approx(a0.x - m);
+            const float w1 = a1.x == -INFINITY ? 0.0f : ex2_approx(a1.x - m);
+            const float l = w0 * a0.y + w1 * a1.y;
+            const bool direct = r.whole && !r.common && s.common < 0;
+            const uint32_t o0 = tmem + lane_base + 256 + t * (D / 2);
+            const int64_t out_row = static_cast<int64_t>(token) * p.heads + head;
+            const int64_t part = r.piece > 0 ? p.rows_cut + static_cast<int64_t>(blockIdx.x) * 128 + row
+                                             : (r.common ? p.rows_common : 0) + out_row;
+            if (busy && has0) {
+                const float inv = direct ? 1.0f / l : 1.0f;
+                uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + t * (D / 2);
+                float4 *prow = reinterpret_cast<float4 *>(p.part_o + part * D + t * (D / 2));
+#pragma unroll 1
+                for (int cb = 0; cb < D / 64; ++cb) {
+                    uint32_t v[32], v1[32];
+                    tmem_ld32(o0 + cb * 32, v);
+                    if (has1) tmem_ld32(o0 + 128 + cb * 32, v1);
+                    tmem_wait_ld_bind(v);
+                    if (has1) {
+                        reg_bind(v1);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __float_as_uint((w0 * __uint_as_float(v[i]) + w1 * __uint_as_float(v1[i])) * inv);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(w0 * __uint_as_float(v[i]) * inv);
+                    }
+                    if (valid && direct) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint4 y;
+                            y.x = pack_16x2<HALF>(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]));
+                            y.y = pack_16x2<HALF>(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]));
+                            y.z = pack_16x2<HALF>(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]));
+                            y.w = pack_16x2<HALF>(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]));
+                            *reinterpret_cast<uint4 *>(orow + cb * 32 + q * 8) = y;
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            prow[cb * 8 + q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                                           __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+                    }
+                }
+            }
+            if (valid && !direct && t == 0) p.part_ml[part] = make_float2(m, l);
+            tc_fence_before();
+            named_bar_sync(1, 256);                  // xm and both accumulators have been read
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Merge of the partial results: a warp per output row (token, head).  Its parts are the
+// pieces of its unit of the stream's own keys and of its unit of the group's common keys;
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  The pieces' (m, l) are read by the
+// lanes at once, then the rows, four in flight.
+template <int D, bool HALF, int kS, int kM>
+__global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    if (*p.v.version != p.v.expect) return;
+    const int lane = threadIdx.x & 31;
+    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (out_row >= static_cast<int64_t>(p.n_queries) * p.heads) return;
+    const int token = static_cast<int>(out_row / p.heads), head = static_cast<int>(out_row - static_cast<int64_t>(token) * p.heads);
+    int lo = p.n_common, hi = p.n_sections;              // the section of the stream's own keys
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.section[mid].token0 <= token)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    // pieces of the row's unit in both sections: CTAs first .. first + n - 1, row in the tile
+    int n[2] = {0, 0}, cta[2], in_tile[2];
+    const int own = lo, common = p.section[lo].common;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k == 1 && common < 0) continue;
+        const PageSection &s = p.section[k ? common : own];
+        const int place = k ? p.section[own].common_token + token - p.section[own].token0 : token - s.token0;
+        const int rt = place / p.tile_tokens;
+        const int64_t a = s.start + (static_cast<int64_t>(rt) * p.v.kv_heads + head / p.group) * s.tiles;
+        cta[k] = static_cast<int>(((a + 1) * p.n_ctas - 1) / p.n_tiles);
+        n[k] = static_cast<int>(((a + s.tiles) * p.n_ctas - 1) / p.n_tiles) - cta[k] + 1;
+        in_tile[k] = (place - rt * p.tile_tokens) * p.group + head % p.group;
+    }
+    const int total = n[0] + n[1];
+    if (total == 1) return;                              // written by the attention kernel
+    auto part_row = [&](int i) -> int64_t {              // i-th part
+        const bool k = i >= n[0];
+        const int piece = k ? i - n[0] : i;
+        if (piece == 0) return (k ? p.rows_common : 0) + out_row;
+        return p.rows_cut + static_cast<int64_t>((k ? cta[1] : cta[0]) + piece) * 128 + (k ? in_tile[1] : in_tile[0]);
+    };
+    float m = -INFINITY, l = 0.0f;
+    float acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
+    for (int i0 = 0; i0 < total; i0 += 32) {
+        const float2 ml = i0 + lane < total ? p.part_ml[part_row(i0 + lane)] : make_float2(-INFINITY, 0.0f);
+        float mb = ml.x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
+        mb = fmaxf(mb, m);
+        const float c = m == -INFINITY ? 0.0f : exp2f(m - mb);
+        l *= c;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] *= c;
+        const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mb);
+        float lw = w * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        l += lw;
+        m = mb;
+        const int nb = min(32, total - i0);
+        for (int g = 0; g < nb; g += 4) {
+            float x[4][D / 32];
+            float wj[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                wj[j] = __shfl_sync(0xffffffffu, w, (g + j) & 31);
+                if (g + j >= nb) wj[j] = 0.0f;
+                if (wj[j] != 0.0f) {                     // (a part without keys has no output row)
+                    const float *src = p.part_o + part_row(i0 + g + j) * D + lane * (D / 32);
+                    if constexpr (D == 128)
+                        *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(src);
+                    else
+                        *reinterpret_cast<float2 *>(x[j]) = *reinterpret_cast<const float2 *>(src);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) x[j][i] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) acc[i] += wj[j] * x[j][i];
+        }
+    }
+    const float inv = 1.0f / l;
+    uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * (D / 32);
+    if constexpr (D == 128)
+        *reinterpret_cast<uint2 *>(orow) =
+            make_uint2(pack_16x2<HALF>(acc[0] * inv, acc[1] * inv), pack_16x2<HALF>(acc[2] * inv, acc[3] * inv));
+    else
+        *reinterpret_cast<uint32_t *>(orow) = pack_16x2<HALF>(acc[0] * inv, acc[1] * inv);
+}
+
+template <int D, bool HALF, int kS, int kM>
+static cudaError_t launch_d(const PagesAttnParams<kS, kM> &p, const CUtensorMap &tk, const CUtensorMap &tv, bool merge,
+                            cudaStream_t s) {
+    static std::atomic<uint64_t> configured{0};          // (per device)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        e = cudaFuncSetAttribute(pages_attention_kernel<D, HALF, kS, kM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 PagesLayout<D>::kAlloc);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    e = launch_dependent(pages_attention_kernel<D, HALF, kS, kM>, dim3(p.n_ctas), dim3(kAttnThreads),
+                         static_cast<size_t>(PagesLayout<D>::kAlloc), s, p, tk, tv);
+    if (e != cudaSuccess || !merge) return e;
+    const int64_t rows = static_cast<int64_t>(p.n_queries) * p.heads;
+    return launch_dependent(pages_merge_kernel<D, HALF, kS, kM>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256),
+                            0, s, p);
+}
+
+template <int kS, int kM>
+cudaError_t launch_pages_attention(const PagesAttnParams<kS, kM> &p, const CUtensorMap &tk, const CUtensorMap &tv,
+                                   bool half, bool merge, cudaStream_t s) {
+    if (p.v.head_dim == 64)
+        return half ? launch_d<64, true>(p, tk, tv, merge, s) : launch_d<64, false>(p, tk, tv, merge, s);
+    return half ? launch_d<128, true>(p, tk, tv, merge, s) : launch_d<128, false>(p, tk, tv, merge, s);
+}
+
+template cudaError_t launch_pages_attention(const PagesAttnParams<kSmallSections, kSmallMembers> &, const CUtensorMap &,
+                                            const CUtensorMap &, bool, bool, cudaStream_t);
+template cudaError_t launch_pages_attention(const PagesAttnParams<kLargeSections, kLargeMembers> &, const CUtensorMap &,
+                                            const CUtensorMap &, bool, bool, cudaStream_t);
+
+}  // namespace sdv2

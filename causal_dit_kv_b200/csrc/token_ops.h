@@ -31,4 +31,103 @@ cudaError_t launch_prompt(const PromptParams<kItems> &p, const CUtensorMap &tq, 
 // Reads and clears the device word in which the prompt kernels record waits that ran out.
 cudaError_t prompt_status(uint32_t *word);
 
+// ---------------------------------------------------------------- paged cache
+constexpr int kPagesMaxStreams = 256;
+constexpr int kPagesMaxCtas = 160;        // attention CTAs of one call, at most (scratch is sized for them)
+
+// Status bits of the paged cache's word besides the waits of sdv2_internal.h.
+constexpr uint32_t kStatusStale = 1u << 5;   // a replayed call whose tables have been forked, freed or compacted since
+
+// Device state that every kernel of a handle takes.
+struct PagesView {
+    int32_t *table;                       // [streams][width], -1 behind a stream's pages
+    int32_t *lengths;                     // [streams]
+    uint32_t *version;                    // and the version that the call was made for
+    uint32_t *status;
+    uint32_t expect;
+    int32_t width, pages, kv_heads, page_log2, head_dim;
+};
+
+// Edits of the tables: rows copied (entries 0 .. n - 1 of a stream's row to another's), row
+// ends set to -1, entries and lengths set.  One launch's edits touch different entries.
+template <int kEntries, int kRows>
+struct PageEdits {
+    int32_t *table, *lengths;
+    uint32_t *version;
+    uint32_t new_version;
+    int32_t width, n_copies, n_clears, n_entries, n_lengths;
+    int32_t copy[kRows][3];               // from, to, entries
+    int32_t clear[kRows][2];              // stream, entries
+    uint32_t entry_at[kEntries];
+    int32_t entry[kEntries];
+    int32_t length[kRows][2];             // stream, tokens
+};
+
+// Pages copied in every layer: source i goes to dst[first[i] .. first[i + 1] - 1].
+template <int kMoves>
+struct PageMoves {
+    uint8_t *base[2];                     // keys and values
+    int64_t layer_stride, page_bytes;
+    int32_t layers, n;
+    int32_t src[kMoves];
+    int32_t first[kMoves + 1];
+    int32_t dst[kMoves];
+};
+
+// New tokens' keys and values: token x of the call belongs to active stream i with
+// first[i] <= x < first[i + 1].
+struct PageWriteParams {
+    PagesView v;
+    const uint16_t *in[2];
+    uint16_t *out[2];                     // this layer's keys and values
+    int64_t stride[2];
+    int32_t n;
+    int32_t stream[kPagesMaxStreams];
+    int32_t first[kPagesMaxStreams + 1];
+};
+
+// One part of the attention's work: the keys of a group's common pages with the queries of
+// all its streams, or a stream's remaining keys with its own queries.  Units (row tile,
+// key head) of `tiles` KV tiles each, numbered row tile first.
+struct PageSection {
+    int32_t start;                        // place of its first tile among all the call's tiles
+    int32_t tiles;
+    int32_t stream;                       // whose table row names the pages
+    int32_t page0;                        // first page of the keys
+    int32_t keys;                         // common pages: their tokens; a stream's own: -1 (up to its length)
+    int32_t token0, n_tokens;             // queries: packed tokens (own keys), or places in the groups' token order
+    int32_t common, common_token;         // own keys: section of the common pages (-1: none), the first query's place there
+};
+
+template <int kSections, int kMembers>
+struct PagesAttnParams {
+    PagesView v;
+    const uint16_t *q;
+    uint16_t *out;
+    int64_t q_stride, out_stride;
+    float *part_o;                        // [rows][d] unnormalised partial outputs
+    float2 *part_ml;                      // [rows] (row maximum in log2 units, row sum)
+    int32_t rows_common, rows_cut;        // first partial row of the common pages' pieces, of the pieces cut by a CTA border
+    int32_t heads, group, tile_tokens, block;
+    int32_t n_sections, n_common, n_tiles, n_ctas, n_queries;
+    float scale_log2;
+    // groups' token order: member i is packed tokens member_token[i] .., at places member_first[i] ..
+    int32_t n_members;
+    int32_t member_first[kMembers];
+    int32_t member_token[kMembers];
+    PageSection section[kSections];       // the groups' common pages, then the streams by their packed tokens
+};
+
+constexpr int kSmallSections = 40, kSmallMembers = 40;
+constexpr int kLargeSections = kPagesMaxStreams + kPagesMaxStreams / 2, kLargeMembers = kPagesMaxStreams;
+
+template <int kEntries, int kRows>
+cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, cudaStream_t s);
+template <int kMoves>
+cudaError_t launch_page_moves(const PageMoves<kMoves> &m, cudaStream_t s);
+cudaError_t launch_page_write(const PageWriteParams &p, cudaStream_t s);
+template <int kSections, int kMembers>
+cudaError_t launch_pages_attention(const PagesAttnParams<kSections, kMembers> &p, const CUtensorMap &tk,
+                                   const CUtensorMap &tv, bool half, bool merge, cudaStream_t s);
+
 }  // namespace sdv2

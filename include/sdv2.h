@@ -422,6 +422,131 @@ sdv2_status sdv2_prompt_attention(const sdv2_prompt_config *cfg, const void *q, 
  * their bound (SDV2_E_DEVICE; the record is cleared). */
 sdv2_status sdv2_prompt_check(void);
 
+/* ------------------------------------------------------------------------
+ * Paged cache: streams that keep all their tokens, in pages of one pool.
+ * ---------------------------------------------------------------------- */
+
+typedef struct {
+    int32_t streams;        /* 1..256; each starts empty */
+    int32_t layers;
+    int32_t heads;          /* Hq: query heads, a multiple of kv_heads; Hq / Hkv <= 128 */
+    int32_t kv_heads;       /* Hkv: query head h reads key head h / (Hq / Hkv) */
+    int32_t head_dim;       /* d: 64 or 128 */
+    int32_t page_tokens;    /* n: tokens of a page: 16, 32, 64 or 128 */
+    int32_t pages;          /* P: pages of the pool (a page holds its tokens in every layer) */
+    int32_t stream_pages;   /* pages that one stream can have, at most; x page_tokens < 2^30 */
+    int32_t max_queries;    /* query tokens of one attention call, all streams together */
+    int32_t block_tokens;   /* b >= 1: attention is causal by blocks of b tokens (1: token by token) */
+    int32_t dtype;          /* SDV2_DT_BF16 or SDV2_DT_FP16 */
+} sdv2_pages_config;
+
+typedef struct sdv2_pages sdv2_pages;
+
+/* Byte offsets inside the caller's pool buffer (all 256-byte aligned). */
+typedef struct {
+    uint64_t k_offset;      /* keys, [L][P][Hkv][n][d] */
+    uint64_t v_offset;      /* values, the same */
+    uint64_t layer_stride;  /* bytes between layers of the keys (and of the values) */
+    uint64_t table_offset;  /* int32 [streams][stream_pages]: each stream's pages in order, then -1 */
+    uint64_t length_offset; /* int32 [streams]: tokens of each stream */
+    uint64_t version_offset; /* uint32: counts the calls that fork, free or compact */
+    uint64_t status_offset; /* uint32: device status word (0 = ok) */
+    uint64_t scratch_offset; /* partial results of the attention */
+    uint64_t scratch_bytes;
+    uint64_t total_bytes;   /* == sdv2_pages_bytes(cfg) */
+} sdv2_pages_layout;
+
+/* Device bytes the caller must allocate for a pool with this config; 0 if the config is
+ * invalid (see sdv2_last_error). */
+size_t sdv2_pages_bytes(const sdv2_pages_config *cfg);
+
+/* Fill *out with the region offsets of a pool buffer for cfg. */
+sdv2_status sdv2_pages_layout_of(const sdv2_pages_config *cfg, sdv2_pages_layout *out);
+
+/* Bind a handle to the caller's device buffer (256-byte aligned, >= sdv2_pages_bytes) on
+ * the current device.  Zero-fills the buffer, synchronously.
+ *
+ * The handle keeps every stream's page list, the tokens of each and the users of each page
+ * on the host; the device's tables follow in stream order.  So the calls of one handle belong
+ * on one stream, or on streams that the caller orders, and from one thread at a time; the
+ * attention's scratch is shared by all its calls.
+ * CUDA graphs: sdv2_pages_write and sdv2_pages_attention can be captured.  A replay takes the
+ * streams' lengths and pages of the time of the replay (as sdv2_pages_extend left them; the
+ * captured split of the work stays right, though not as even, as streams grow).  A replay
+ * after a fork, free or compact of the handle does nothing but set the status word
+ * (sdv2_pages_check): capture again.  The calls that change the tables are refused
+ * (SDV2_E_STATE) on a stream in capture.
+ * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN, SDV2_E_CUDA. */
+sdv2_status sdv2_pages_create(const sdv2_pages_config *cfg, void *dev_buf, size_t bytes, sdv2_pages **out);
+
+/* Release the host handle.  The device buffer is the caller's to free. */
+sdv2_status sdv2_pages_destroy(sdv2_pages *pages);
+
+/* counts: HOST int32 [streams], >= 0.  Stream b becomes counts[b] tokens longer, taking the
+ * lowest free pages in order (stream by stream).  The new tokens' keys and values are what
+ * sdv2_pages_write puts there, layer by layer.
+ * Errors: SDV2_E_ARG; SDV2_E_STATE without enough free pages, past stream_pages, or in
+ * capture (nothing has changed then); SDV2_E_CUDA. */
+sdv2_status sdv2_pages_extend(sdv2_pages *pages, const int32_t *counts, sdv2_stream stream);
+
+/* Keys and values of the last counts[b] tokens of each stream b, in one layer.
+ * k, v: device [sum counts][Hkv][d], streams in order; k_stride, v_stride: elements between
+ *   tokens (multiples of 8; 0: contiguous).  counts: HOST int32 [streams], >= 0.
+ * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN; SDV2_E_STATE if a stream has fewer tokens
+ * or one of those lies in a page that streams share; SDV2_E_CUDA. */
+sdv2_status sdv2_pages_write(sdv2_pages *pages, int32_t layer, const void *k, const void *v, int64_t k_stride,
+                             int64_t v_stride, const int32_t *counts, sdv2_stream stream);
+
+/* Attention of the last counts[b] tokens of each stream b over the stream's keys of one
+ * layer: out_i = sum_j softmax_j(softmax_scale * q_i . k_j) v_j over j with
+ * floor(j / b) <= floor(i / b), i and j counted from the stream's start.
+ * q, out: device [sum counts][Hq][d], streams in order; q_stride, out_stride: elements
+ *   between tokens (multiples of 8; 0: contiguous).  counts: HOST int32 [streams], >= 0 (0:
+ *   the stream takes no part), their sum at most max_queries.  out overlaps no input.
+ * Streams that share their leading pages (sdv2_pages_fork) have those read and multiplied
+ * once for all of them: one group per first page, over the pages that all its streams have in
+ * common.  Roundings as in sdv2_prompt_attention; what a page holds behind its stream's
+ * last token has no part in the result.
+ * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN; SDV2_E_STATE if a stream has fewer
+ * tokens; SDV2_E_CUDA. */
+sdv2_status sdv2_pages_attention(sdv2_pages *pages, int32_t layer, const void *q, void *out, int64_t q_stride,
+                                 int64_t out_stride, const int32_t *counts, float softmax_scale,
+                                 sdv2_stream stream);
+
+/* The empty streams dst[0..n-1] become copies of stream src.  deep 0: they share its full
+ * pages, and its last page, if it is not full, is copied for each; deep 1: every page is
+ * copied.  All layers; the copies take the lowest free pages in order.
+ * Errors: SDV2_E_ARG (a stream out of range, src or a stream twice among dst);
+ * SDV2_E_STATE (a dst that is not empty, too few free pages, capture; nothing has changed
+ * then); SDV2_E_CUDA. */
+sdv2_status sdv2_pages_fork(sdv2_pages *pages, int32_t src, const int32_t *dst, int32_t n, int32_t deep,
+                            sdv2_stream stream);
+
+/* The given streams (each once) become empty; pages that no stream uses are free again.
+ * Errors: SDV2_E_ARG, SDV2_E_STATE (capture), SDV2_E_CUDA. */
+sdv2_status sdv2_pages_free(sdv2_pages *pages, const int32_t *streams, int32_t n, sdv2_stream stream);
+
+/* Moves pages so that the used ones are 0 .. used - 1 (*used, if not NULL): the used pages
+ * from `used` on go, in order, to the free ones below it, in order.  All layers.
+ * Errors: SDV2_E_ARG, SDV2_E_STATE (capture), SDV2_E_CUDA. */
+sdv2_status sdv2_pages_compact(sdv2_pages *pages, int32_t *used, sdv2_stream stream);
+
+/* Host bookkeeping of one stream: its tokens, its pages (up to `capacity` of them into
+ * page_ids, which may be NULL with capacity 0), their number, and how many leading pages
+ * it has in common with all streams of its group (0: it shares none). */
+sdv2_status sdv2_pages_query(sdv2_pages *pages, int32_t stream, int32_t *tokens, int32_t *page_ids, int32_t capacity,
+                             int32_t *n_pages, int32_t *shared_pages);
+
+/* Used pages of the pool. */
+int32_t sdv2_pages_used(const sdv2_pages *pages);
+
+sdv2_status sdv2_pages_layout_get(const sdv2_pages *pages, sdv2_pages_layout *out);
+
+/* Synchronise the device and read the status word: SDV2_E_DEVICE (and the word is
+ * cleared) after a wait that ran past its bound, or a replay of a captured call that the
+ * tables had outgrown. */
+sdv2_status sdv2_pages_check(sdv2_pages *pages);
+
 /* Kernels launched by this library in this process so far. */
 uint64_t sdv2_launch_count(void);
 /* Thread-local message describing the last failing call ("" if none). */
