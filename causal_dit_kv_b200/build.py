@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsdv2.so")
 SOURCES = ["host.cpp", "append.cu", "attention.cu", "refresh.cu", "motion.cu", "motion_noalloc.cu",
-           "host_prompt.cpp", "prompt.cu", "host_pages.cpp", "pages.cu", "pages_attention.cu"]
+           "host_prompt.cpp", "prompt.cu", "host_pages.cpp", "pages.cu", "pages_attention.cu", "pages_rows.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

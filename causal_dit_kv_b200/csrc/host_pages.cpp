@@ -18,11 +18,11 @@ struct Regions {
 };
 
 // Rows of the attention's partial results: one of the stream's own keys and one of the
-// group's common keys per (query token, head), and 128 per CTA for a piece whose unit began
-// in an earlier CTA.
-int64_t partial_rows(const sdv2_pages_config &c) {
-    return 2ll * c.max_queries * c.heads + static_cast<int64_t>(kPagesMaxCtas) * 128;
-}
+// group's common keys per (query token, head), and for each of the call's two launches those
+// of every worker's piece whose unit began with an earlier worker.
+constexpr int32_t kCutRows = kPagesMaxCtas * 128;
+static_assert(kCutRows == kPagesMaxCtas * kRowWarps * kRowsPerWorker, "the same for both kernels");
+int64_t partial_rows(const sdv2_pages_config &c) { return 2ll * c.max_queries * c.heads + 2 * kCutRows; }
 
 Regions regions(const sdv2_pages_config &c) {
     Regions r{};
@@ -389,7 +389,18 @@ sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, in
     return SDV2_OK;
 }
 
-// The sections of one attention call, and whether any row's result comes in parts.
+// Whether the launch leaves any unit in pieces: a worker border inside one.
+template <typename P>
+bool cuts_units(const P &p, const PageWork &w) {
+    for (int worker = 1, i = w.begin; worker < w.workers; ++worker) {
+        const int64_t pos = static_cast<int64_t>(worker) * w.tiles / w.workers;
+        while (i + 1 < w.end && p.section[i + 1].start <= pos) ++i;
+        if ((pos - p.section[i].start) % p.section[i].tiles != 0) return true;
+    }
+    return false;
+}
+
+// The sections of one attention call and its launches.
 template <int kS, int kM>
 sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64_t q_stride, int64_t out_stride,
                    const int32_t *counts, int64_t sum, float scale, cudaStream_t s) {
@@ -398,42 +409,34 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
     p->v = h->view();
     p->q = static_cast<const uint16_t *>(q);
     p->out = static_cast<uint16_t *>(out);
+    p->k_layer = reinterpret_cast<const uint16_t *>(h->base + h->r.k + h->r.layer_stride * layer);
+    p->v_layer = reinterpret_cast<const uint16_t *>(h->base + h->r.v + h->r.layer_stride * layer);
     p->q_stride = q_stride;
     p->out_stride = out_stride;
     p->part_ml = reinterpret_cast<float2 *>(h->base + h->r.part_ml);
     p->part_o = reinterpret_cast<float *>(h->base + h->r.part_o);
     p->rows_common = c.max_queries * c.heads;
-    p->rows_cut = 2 * c.max_queries * c.heads;
     p->heads = c.heads;
     p->group = c.heads / c.kv_heads;
-    p->tile_tokens = 128 / p->group;
     p->block = c.block_tokens;
     p->scale_log2 = scale * 1.4426950408889634f;
     p->n_queries = static_cast<int32_t>(sum);
 
     int32_t token_of[kPagesMaxStreams];   // first packed token of each stream
-    int32_t at = 0;
+    int32_t at = 0, most_tokens = 0;
     for (int32_t b = 0; b < c.streams; ++b) {
         token_of[b] = at;
         at += counts[b];
+        most_tokens = std::max(most_tokens, counts[b]);
     }
-    int64_t tiles = 0;
-    int n = 0;
-    auto add = [&](int32_t n_tokens, int64_t keys) -> PageSection & {
-        PageSection &x = p->section[n++];
-        x.start = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
-        x.tiles = static_cast<int32_t>((keys + 127) / 128);
-        x.n_tokens = n_tokens;
-        tiles += static_cast<int64_t>((n_tokens + p->tile_tokens - 1) / p->tile_tokens) * c.kv_heads * x.tiles;
-        return x;
-    };
     // groups of active streams with common leading pages: every query sees all of those keys
     know_groups(h);
     const int n_groups = static_cast<int>(h->group_pages.size());
     int32_t section_of[kPagesMaxStreams];                    // of each group in this call (-1: none)
     int32_t place_of[kPagesMaxStreams];                      // first query's place of a stream among its section's
     p->n_members = 0;
-    int32_t member_at = 0;
+    int n = 0;
+    int32_t member_at = 0, most_common = 0;
     for (int g = 0; g < n_groups; ++g) {
         section_of[g] = -1;
         int32_t members = 0, group_tokens = 0, first = -1;
@@ -447,13 +450,15 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
         }
         if (members < 2 || pages < 1) continue;
         section_of[g] = n;
-        PageSection &x = add(group_tokens, static_cast<int64_t>(pages) * c.page_tokens);
+        PageSection &x = p->section[n++];
         x.stream = first;
         x.page0 = 0;
         x.keys = pages * c.page_tokens;
         x.token0 = member_at;
+        x.n_tokens = group_tokens;
         x.common = -1;
         x.common_token = 0;
+        most_common = std::max(most_common, group_tokens);
         int32_t place = 0;
         for (int32_t b = 0; b < c.streams; ++b) {
             if (h->group_of[b] != g || counts[b] == 0) continue;
@@ -468,32 +473,65 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
     for (int32_t b = 0; b < c.streams; ++b) {
         if (counts[b] == 0) continue;
         const int32_t common = h->group_of[b] >= 0 ? section_of[h->group_of[b]] : -1;
-        const int32_t page0 = common >= 0 ? p->section[common].keys / c.page_tokens : 0;
-        PageSection &x = add(counts[b], static_cast<int64_t>(h->tokens[b]) - static_cast<int64_t>(page0) * c.page_tokens);
+        PageSection &x = p->section[n++];
         x.stream = b;
-        x.page0 = page0;
+        x.page0 = common >= 0 ? p->section[common].keys / c.page_tokens : 0;
         x.keys = -1;
         x.token0 = token_of[b];
+        x.n_tokens = counts[b];
         x.common = common;
         x.common_token = common >= 0 ? place_of[b] : 0;
     }
     p->n_sections = n;
-    if (tiles >= (1ll << 31) / kPagesMaxCtas * 100) return fail(SDV2_E_SHAPE, "too much work for one call");
-    p->n_tiles = static_cast<int32_t>(tiles);
-    p->n_ctas = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>({h->sm_count, kPagesMaxCtas, (tiles + 1) / 2})));
 
-    // parts to merge: common pages, or a CTA border inside a unit
-    bool merge = p->n_common > 0;
-    for (int cta = 1, i = 0; !merge && cta < p->n_ctas; ++cta) {
-        const int64_t pos = static_cast<int64_t>(cta) * tiles / p->n_ctas;
-        while (i + 1 < n && p->section[i + 1].start <= pos) ++i;
-        merge = (pos - p->section[i].start) % p->section[i].tiles != 0;
+    // Both parts' kernels: a warp per run where no unit has more than 16 rows.  (The groups'
+    // units have at least as many rows as their streams'.)
+    const bool few_own = static_cast<int64_t>(most_tokens) * p->group <= kRowsPerWorker;
+    const bool few_common = static_cast<int64_t>(most_common) * p->group <= kRowsPerWorker;
+    auto work = [&](int begin, int end, bool few, int32_t cut_row) {
+        PageWork w{};
+        w.begin = begin;
+        w.end = end;
+        w.tile_log2 = few ? 4 : 7;
+        w.tile_tokens = (few ? kRowsPerWorker : 128) / p->group;
+        w.cut_row = cut_row;
+        w.cut_rows = few ? kRowsPerWorker : 128;
+        int64_t tiles = 0;
+        for (int i = begin; i < end; ++i) {
+            PageSection &x = p->section[i];
+            const int64_t keys = x.keys >= 0 ? x.keys : h->tokens[x.stream] - static_cast<int64_t>(x.page0) * c.page_tokens;
+            x.start = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
+            x.tiles = static_cast<int32_t>((keys + (1 << w.tile_log2) - 1) >> w.tile_log2);
+            tiles += static_cast<int64_t>((x.n_tokens + w.tile_tokens - 1) / w.tile_tokens) * c.kv_heads * x.tiles;
+        }
+        w.tiles = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
+        const int64_t most = static_cast<int64_t>(std::min(h->sm_count, kPagesMaxCtas)) * (few ? kRowWarps : 1);
+        const int64_t shortest = few ? 4 : 2;                // tiles of a run, at least
+        w.workers = static_cast<int32_t>(std::max<int64_t>(1, std::min(most, (tiles + shortest - 1) / shortest)));
+        return w;
+    };
+    const int32_t cut = 2 * c.max_queries * c.heads;
+    const bool together = p->n_common == 0 || few_common == few_own;
+    p->own = work(together ? 0 : p->n_common, n, few_own, cut);
+    p->common = together ? p->own : work(0, p->n_common, few_common, cut + kCutRows);
+    if (p->own.tiles == INT32_MAX || p->common.tiles == INT32_MAX) return fail(SDV2_E_SHAPE, "too much work for one call");
+
+    const bool half = c.dtype == SDV2_DT_FP16;
+    cudaError_t e = cudaSuccess;
+    if (!together) {
+        e = launch_pages_tiles<kS, kM>(*p, p->common, h->tk[layer], h->tv[layer], half, s);
+        if (e == cudaSuccess) count_launch();
     }
-    const cudaError_t e = launch_pages_attention<kS, kM>(*p, h->tk[layer], h->tv[layer], c.dtype == SDV2_DT_FP16, merge, s);
-    if (e != cudaSuccess) return cuda_fail(e, "pages_attention launch");
-    count_launch();
-    if (merge) count_launch();
-    return SDV2_OK;
+    if (e == cudaSuccess) {
+        e = few_own ? launch_pages_rows<kS, kM>(*p, p->own, half, !together, h->sm_count, s)
+                    : launch_pages_tiles<kS, kM>(*p, p->own, h->tk[layer], h->tv[layer], half, s);
+        if (e == cudaSuccess) count_launch();
+    }
+    if (e == cudaSuccess && (p->n_common > 0 || cuts_units(*p, p->own))) {
+        e = launch_pages_merge<kS, kM>(*p, half, s);
+        if (e == cudaSuccess) count_launch();
+    }
+    return e == cudaSuccess ? SDV2_OK : cuda_fail(e, "pages_attention launch");
 }
 
 sdv2_status attention(sdv2_pages *h, int32_t layer, const void *q, void *out, int64_t q_stride, int64_t out_stride,

@@ -21,7 +21,7 @@
 #include <atomic>
 
 #include "attn_core.cuh"
-#include "token_ops.h"
+#include "pages_runs.cuh"
 
 namespace sdv2 {
 
@@ -45,83 +45,16 @@ struct PagesLayout {
     static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
 
-// A CTA's run of tiles within one unit.
-struct PagesRun {
-    int sec, row_tile, head;     // section, 128-row tile, key head
-    int n_rows;                  // query rows of the tile
-    int begin, n;                // first KV tile of the run in the unit, tiles (0: nothing to read)
-    int keys;                    // keys of the unit's page range (they end inside its last tile)
-    int base;                    // place in the stream of its first key
-    int len;                     // tokens of the stream
-    int piece;                   // which piece of the unit this is (0: its first)
-    bool whole, common;          // the unit's only piece; keys of common pages
-};
-
-template <int kS, int kM>
-__device__ __forceinline__ PagesRun pages_run(const PagesAttnParams<kS, kM> &p, int pos, int end, int *taken) {
-    int lo = 0, hi = p.n_sections;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.section[mid].start <= pos)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    const PageSection &s = p.section[lo];
-    PagesRun r;
-    r.sec = lo;
-    const int unit = (pos - s.start) / s.tiles;
-    r.begin = pos - s.start - unit * s.tiles;
-    *taken = min(s.tiles - r.begin, end - pos);
-    r.row_tile = unit / p.v.kv_heads;
-    r.head = unit - r.row_tile * p.v.kv_heads;
-    r.common = s.keys >= 0;
-    r.base = s.page0 << p.v.page_log2;
-    r.len = p.v.lengths[s.stream];
-    const int tokens = min(p.tile_tokens, s.n_tokens - r.row_tile * p.tile_tokens);
-    r.n_rows = tokens * p.group;
-    r.keys = r.common ? s.keys : r.len - r.base;
-    // KV tiles that the tile's rows see: all of the common keys, or up to its last token's
-    int tiles = (r.keys + 127) >> 7;
-    if (!r.common) {
-        const int last = r.len - s.n_tokens + r.row_tile * p.tile_tokens + tokens - 1;
-        tiles = (min(r.len, (last / p.block + 1) * p.block) - r.base + 127) >> 7;
-    }
-    // (the unit's last piece takes what a longer stream has grown since the work was cut)
-    const bool last_piece = r.begin + *taken == s.tiles;
-    r.n = max(0, (last_piece ? tiles : min(tiles, r.begin + *taken)) - r.begin);
-    const int64_t first = static_cast<int64_t>(s.start) + static_cast<int64_t>(unit) * s.tiles;
-    r.piece = static_cast<int>(blockIdx.x - ((first + 1) * p.n_ctas - 1) / p.n_tiles);
-    r.whole = r.begin == 0 && last_piece;
-    return r;
-}
-
 // Valid keys of the run's last tile if the range ends inside it (0: it does not).
 __device__ __forceinline__ int tail_keys(const PagesRun &r) {
     const int left = r.keys - (r.begin + r.n - 1) * 128;
     return r.n > 0 && left < 128 ? left : 0;
 }
 
-// Packed token of the `place`-th query token of a section.
-template <int kS, int kM>
-__device__ __forceinline__ int query_token(const PagesAttnParams<kS, kM> &p, const PageSection &s, int place) {
-    if (s.keys < 0) return s.token0 + place;
-    const int x = s.token0 + place;
-    int lo = 0, hi = p.n_members;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.member_first[mid] <= x)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return p.member_token[lo] + x - p.member_first[lo];
-}
-
 template <int D, bool HALF, int kS, int kM>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-    pages_attention_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p, const __grid_constant__ CUtensorMap tmap_k,
-                           const __grid_constant__ CUtensorMap tmap_v) {
+    pages_tiles_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p, const __grid_constant__ PageWork work,
+                       const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v) {
     using L = PagesLayout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -152,8 +85,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     grid_launch_dependents();
 
     // this CTA's tiles (none if the tables are not those of the call)
-    int pos0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.n_tiles / p.n_ctas);
-    int end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.n_tiles / p.n_ctas);
+    int pos0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * work.tiles / work.workers);
+    int end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * work.tiles / work.workers);
     if (*p.v.version != p.v.expect) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kStatusStale);
         end = pos0 = 0;
@@ -170,7 +103,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             int kc = 0, vc = 0;
             bool ok = true;
             for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, pos, end, &taken);
+                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
                 if (r.n == 0) continue;
                 const PageSection &s = p.section[r.sec];
                 const int32_t *row = p.v.table + static_cast<int64_t>(s.stream) * p.v.width + s.page0;
@@ -259,7 +192,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 return true;
             };
             for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, pos, end, &taken);
+                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
                 if (r.n == 0) continue;
                 ok = mbar_wait(&bars[L::kQReady], runs & 1, abort_flag, status, kStatusMmaWait);
                 ++runs;
@@ -305,7 +238,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // ------------------------------------------------ ends of key ranges in V
             int vc = 0, fixes = 0;
             for (int pos = pos0, taken; pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, pos, end, &taken);
+                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
                 vc += r.n;
                 const int valid = tail_keys(r);
                 if (valid == 0) continue;
@@ -326,11 +259,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         int sc = 0, oc[2] = {0, 0};
         bool ok = true;
         for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-            const PagesRun r = pages_run(p, pos, end, &taken);
+            const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
             const PageSection &s = p.section[r.sec];
             const bool valid = row < r.n_rows;
             const bool busy = ((warp & 3) << 5) < r.n_rows;        // the warp has rows
-            const int place = r.row_tile * p.tile_tokens + (valid ? row / p.group : 0);
+            const int place = r.row_tile * work.tile_tokens + (valid ? row / p.group : 0);
             const int head = r.head * p.group + row % p.group;
             const int token = query_token(p, s, place);
             if (r.n > 0) {
@@ -403,8 +336,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const bool direct = r.whole && !r.common && s.common < 0;
             const uint32_t o0 = tmem + lane_base + 256 + t * (D / 2);
             const int64_t out_row = static_cast<int64_t>(token) * p.heads + head;
-            const int64_t part = r.piece > 0 ? p.rows_cut + static_cast<int64_t>(blockIdx.x) * 128 + row
-                                             : (r.common ? p.rows_common : 0) + out_row;
+            const int64_t part = partial_row(p, work, r, blockIdx.x, row, out_row);
             if (busy && has0) {
                 const float inv = direct ? 1.0f / l : 1.0f;
                 uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + t * (D / 2);
@@ -458,136 +390,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Merge of the partial results: a warp per output row (token, head).  Its parts are the
-// pieces of its unit of the stream's own keys and of its unit of the group's common keys;
-// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  The pieces' (m, l) are read by the
-// lanes at once, then the rows, four in flight.
 template <int D, bool HALF, int kS, int kM>
-__global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (*p.v.version != p.v.expect) return;
-    const int lane = threadIdx.x & 31;
-    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (out_row >= static_cast<int64_t>(p.n_queries) * p.heads) return;
-    const int token = static_cast<int>(out_row / p.heads), head = static_cast<int>(out_row - static_cast<int64_t>(token) * p.heads);
-    int lo = p.n_common, hi = p.n_sections;              // the section of the stream's own keys
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.section[mid].token0 <= token)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    // pieces of the row's unit in both sections: CTAs first .. first + n - 1, row in the tile
-    int n[2] = {0, 0}, cta[2], in_tile[2];
-    const int own = lo, common = p.section[lo].common;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        if (k == 1 && common < 0) continue;
-        const PageSection &s = p.section[k ? common : own];
-        const int place = k ? p.section[own].common_token + token - p.section[own].token0 : token - s.token0;
-        const int rt = place / p.tile_tokens;
-        const int64_t a = s.start + (static_cast<int64_t>(rt) * p.v.kv_heads + head / p.group) * s.tiles;
-        cta[k] = static_cast<int>(((a + 1) * p.n_ctas - 1) / p.n_tiles);
-        n[k] = static_cast<int>(((a + s.tiles) * p.n_ctas - 1) / p.n_tiles) - cta[k] + 1;
-        in_tile[k] = (place - rt * p.tile_tokens) * p.group + head % p.group;
-    }
-    const int total = n[0] + n[1];
-    if (total == 1) return;                              // written by the attention kernel
-    auto part_row = [&](int i) -> int64_t {              // i-th part
-        const bool k = i >= n[0];
-        const int piece = k ? i - n[0] : i;
-        if (piece == 0) return (k ? p.rows_common : 0) + out_row;
-        return p.rows_cut + static_cast<int64_t>((k ? cta[1] : cta[0]) + piece) * 128 + (k ? in_tile[1] : in_tile[0]);
-    };
-    float m = -INFINITY, l = 0.0f;
-    float acc[D / 32];
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-    for (int i0 = 0; i0 < total; i0 += 32) {
-        const float2 ml = i0 + lane < total ? p.part_ml[part_row(i0 + lane)] : make_float2(-INFINITY, 0.0f);
-        float mb = ml.x;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
-        mb = fmaxf(mb, m);
-        const float c = m == -INFINITY ? 0.0f : exp2f(m - mb);
-        l *= c;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) acc[i] *= c;
-        const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - mb);
-        float lw = w * ml.y;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
-        l += lw;
-        m = mb;
-        const int nb = min(32, total - i0);
-        for (int g = 0; g < nb; g += 4) {
-            float x[4][D / 32];
-            float wj[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                wj[j] = __shfl_sync(0xffffffffu, w, (g + j) & 31);
-                if (g + j >= nb) wj[j] = 0.0f;
-                if (wj[j] != 0.0f) {                     // (a part without keys has no output row)
-                    const float *src = p.part_o + part_row(i0 + g + j) * D + lane * (D / 32);
-                    if constexpr (D == 128)
-                        *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(src);
-                    else
-                        *reinterpret_cast<float2 *>(x[j]) = *reinterpret_cast<const float2 *>(src);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) x[j][i] = 0.0f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) acc[i] += wj[j] * x[j][i];
-        }
-    }
-    const float inv = 1.0f / l;
-    uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * (D / 32);
-    if constexpr (D == 128)
-        *reinterpret_cast<uint2 *>(orow) =
-            make_uint2(pack_16x2<HALF>(acc[0] * inv, acc[1] * inv), pack_16x2<HALF>(acc[2] * inv, acc[3] * inv));
-    else
-        *reinterpret_cast<uint32_t *>(orow) = pack_16x2<HALF>(acc[0] * inv, acc[1] * inv);
-}
-
-template <int D, bool HALF, int kS, int kM>
-static cudaError_t launch_d(const PagesAttnParams<kS, kM> &p, const CUtensorMap &tk, const CUtensorMap &tv, bool merge,
-                            cudaStream_t s) {
+static cudaError_t launch_d(const PagesAttnParams<kS, kM> &p, const PageWork &w, const CUtensorMap &tk,
+                            const CUtensorMap &tv, cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};          // (per device)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(pages_attention_kernel<D, HALF, kS, kM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(pages_tiles_kernel<D, HALF, kS, kM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  PagesLayout<D>::kAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    e = launch_dependent(pages_attention_kernel<D, HALF, kS, kM>, dim3(p.n_ctas), dim3(kAttnThreads),
-                         static_cast<size_t>(PagesLayout<D>::kAlloc), s, p, tk, tv);
-    if (e != cudaSuccess || !merge) return e;
-    const int64_t rows = static_cast<int64_t>(p.n_queries) * p.heads;
-    return launch_dependent(pages_merge_kernel<D, HALF, kS, kM>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256),
-                            0, s, p);
+    return launch_dependent(pages_tiles_kernel<D, HALF, kS, kM>, dim3(w.workers), dim3(kAttnThreads),
+                            static_cast<size_t>(PagesLayout<D>::kAlloc), s, p, w, tk, tv);
 }
 
 template <int kS, int kM>
-cudaError_t launch_pages_attention(const PagesAttnParams<kS, kM> &p, const CUtensorMap &tk, const CUtensorMap &tv,
-                                   bool half, bool merge, cudaStream_t s) {
-    if (p.v.head_dim == 64)
-        return half ? launch_d<64, true>(p, tk, tv, merge, s) : launch_d<64, false>(p, tk, tv, merge, s);
-    return half ? launch_d<128, true>(p, tk, tv, merge, s) : launch_d<128, false>(p, tk, tv, merge, s);
+cudaError_t launch_pages_tiles(const PagesAttnParams<kS, kM> &p, const PageWork &w, const CUtensorMap &tk,
+                               const CUtensorMap &tv, bool half, cudaStream_t s) {
+    if (p.v.head_dim == 64) return half ? launch_d<64, true>(p, w, tk, tv, s) : launch_d<64, false>(p, w, tk, tv, s);
+    return half ? launch_d<128, true>(p, w, tk, tv, s) : launch_d<128, false>(p, w, tk, tv, s);
 }
 
-template cudaError_t launch_pages_attention(const PagesAttnParams<kSmallSections, kSmallMembers> &, const CUtensorMap &,
-                                            const CUtensorMap &, bool, bool, cudaStream_t);
-template cudaError_t launch_pages_attention(const PagesAttnParams<kLargeSections, kLargeMembers> &, const CUtensorMap &,
-                                            const CUtensorMap &, bool, bool, cudaStream_t);
+template cudaError_t launch_pages_tiles(const PagesAttnParams<kSmallSections, kSmallMembers> &, const PageWork &,
+                                        const CUtensorMap &, const CUtensorMap &, bool, cudaStream_t);
+template cudaError_t launch_pages_tiles(const PagesAttnParams<kLargeSections, kLargeMembers> &, const PageWork &,
+                                        const CUtensorMap &, const CUtensorMap &, bool, cudaStream_t);
 
 }  // namespace sdv2

@@ -1,0 +1,91 @@
+// How the paged attention's work is cut: the run of tiles that a worker (a CTA of the
+// tile kernel, a warp of the row kernel) takes within one unit, and where partial results go.
+#pragma once
+
+#include "ptx.cuh"
+#include "token_ops.h"
+
+namespace sdv2 {
+
+struct PagesRun {
+    int sec, row_tile, head;     // section, row tile, key head
+    int n_rows;                  // query rows of the tile
+    int begin, n;                // first KV tile of the run in the unit, tiles (0: nothing to read)
+    int keys;                    // keys of the unit's page range (they end inside its last tile)
+    int base;                    // place in the stream of its first key
+    int len;                     // tokens of the stream
+    int piece;                   // which piece of the unit this is (0: its first)
+    bool whole, common;          // the unit's only piece; keys of common pages
+};
+
+// Worker that takes tile `pos`: the last one whose run begins at or before it, runs beginning
+// at floor(worker * tiles / workers).
+__device__ __forceinline__ int worker_of(const PageWork &w, int64_t pos) {
+    return static_cast<int>(((pos + 1) * w.workers - 1) / w.tiles);
+}
+
+template <int kS, int kM>
+__device__ __forceinline__ PagesRun pages_run(const PagesAttnParams<kS, kM> &p, const PageWork &w, int worker, int pos,
+                                              int end, int *taken) {
+    int lo = w.begin, hi = w.end;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.section[mid].start <= pos)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const PageSection &s = p.section[lo];
+    PagesRun r;
+    r.sec = lo;
+    const int unit = (pos - s.start) / s.tiles;
+    r.begin = pos - s.start - unit * s.tiles;
+    *taken = min(s.tiles - r.begin, end - pos);
+    r.row_tile = unit / p.v.kv_heads;
+    r.head = unit - r.row_tile * p.v.kv_heads;
+    r.common = s.keys >= 0;
+    r.base = s.page0 << p.v.page_log2;
+    r.len = p.v.lengths[s.stream];
+    const int tokens = min(w.tile_tokens, s.n_tokens - r.row_tile * w.tile_tokens);
+    r.n_rows = tokens * p.group;
+    r.keys = r.common ? s.keys : r.len - r.base;
+    // KV tiles that the tile's rows see: all of the common keys, or up to its last token's
+    int seen = r.keys;
+    if (!r.common) {
+        const int last = r.len - s.n_tokens + r.row_tile * w.tile_tokens + tokens - 1;
+        seen = min(r.len, (last / p.block + 1) * p.block) - r.base;
+    }
+    const int tiles = (seen + (1 << w.tile_log2) - 1) >> w.tile_log2;
+    // (the unit's last piece takes what a longer stream has grown since the work was cut)
+    const bool last_piece = r.begin + *taken == s.tiles;
+    r.n = max(0, (last_piece ? tiles : min(tiles, r.begin + *taken)) - r.begin);
+    r.piece = r.begin == 0 ? 0 : worker - worker_of(w, pos - r.begin);
+    r.whole = r.begin == 0 && last_piece;
+    return r;
+}
+
+// Packed token of the `place`-th query token of a section.
+template <int kS, int kM>
+__device__ __forceinline__ int query_token(const PagesAttnParams<kS, kM> &p, const PageSection &s, int place) {
+    if (s.keys < 0) return s.token0 + place;
+    const int x = s.token0 + place;
+    int lo = 0, hi = p.n_members;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.member_first[mid] <= x)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return p.member_token[lo] + x - p.member_first[lo];
+}
+
+// Partial row of the run's tile row `row`, whose output row is out_row.
+template <int kS, int kM>
+__device__ __forceinline__ int64_t partial_row(const PagesAttnParams<kS, kM> &p, const PageWork &w, const PagesRun &r,
+                                               int worker, int row, int64_t out_row) {
+    return r.piece > 0 ? w.cut_row + static_cast<int64_t>(worker) * w.cut_rows + row
+                       : (r.common ? p.rows_common : 0) + out_row;
+}
+
+}  // namespace sdv2

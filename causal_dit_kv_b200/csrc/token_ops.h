@@ -33,7 +33,9 @@ cudaError_t prompt_status(uint32_t *word);
 
 // ---------------------------------------------------------------- paged cache
 constexpr int kPagesMaxStreams = 256;
-constexpr int kPagesMaxCtas = 160;        // attention CTAs of one call, at most (scratch is sized for them)
+constexpr int kPagesMaxCtas = 160;        // attention CTAs of one launch, at most (scratch is sized for them)
+constexpr int kRowWarps = 8;              // warps of a CTA of the few-row kernel, each a worker of its own
+constexpr int kRowsPerWorker = 16;        // query rows that one of them takes, at most
 
 // Status bits of the paged cache's word besides the waits of sdv2_internal.h.
 constexpr uint32_t kStatusStale = 1u << 5;   // a replayed call whose tables have been forked, freed or compacted since
@@ -90,7 +92,7 @@ struct PageWriteParams {
 // all its streams, or a stream's remaining keys with its own queries.  Units (row tile,
 // key head) of `tiles` KV tiles each, numbered row tile first.
 struct PageSection {
-    int32_t start;                        // place of its first tile among all the call's tiles
+    int32_t start;                        // place of its first tile among all the launch's tiles
     int32_t tiles;
     int32_t stream;                       // whose table row names the pages
     int32_t page0;                        // first page of the keys
@@ -99,18 +101,27 @@ struct PageSection {
     int32_t common, common_token;         // own keys: section of the common pages (-1: none), the first query's place there
 };
 
+// One launch's work: sections [begin, end), their units laid end to end in tiles of
+// 1 << tile_log2 keys and cut evenly into `workers` runs; a unit's later pieces leave their
+// rows at partial row cut_row + worker * cut_rows.
+struct PageWork {
+    int32_t begin, end, tiles, workers, tile_log2, tile_tokens, cut_row, cut_rows;
+};
+
 template <int kSections, int kMembers>
 struct PagesAttnParams {
     PagesView v;
     const uint16_t *q;
     uint16_t *out;
+    const uint16_t *k_layer, *v_layer;
     int64_t q_stride, out_stride;
     float *part_o;                        // [rows][d] unnormalised partial outputs
     float2 *part_ml;                      // [rows] (row maximum in log2 units, row sum)
-    int32_t rows_common, rows_cut;        // first partial row of the common pages' pieces, of the pieces cut by a CTA border
-    int32_t heads, group, tile_tokens, block;
-    int32_t n_sections, n_common, n_tiles, n_ctas, n_queries;
+    int32_t rows_common;                  // first partial row of the common pages' pieces
+    int32_t heads, group, block;
+    int32_t n_sections, n_common, n_queries;
     float scale_log2;
+    PageWork common, own;                 // the launches that take the common pages' sections and the streams'
     // groups' token order: member i is packed tokens member_token[i] .., at places member_first[i] ..
     int32_t n_members;
     int32_t member_first[kMembers];
@@ -126,8 +137,16 @@ cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, cudaStream_t 
 template <int kMoves>
 cudaError_t launch_page_moves(const PageMoves<kMoves> &m, cudaStream_t s);
 cudaError_t launch_page_write(const PageWriteParams &p, cudaStream_t s);
+// The work w of a call by 128-row tiles on the tensor cores' own kernel (tiles of 128 keys),
+// or by at most kRowsPerWorker rows of one warp each (tiles of 16 keys).  `beside`: the launch
+// before it in the stream is the same call's other one, which it need not wait for to begin.
 template <int kSections, int kMembers>
-cudaError_t launch_pages_attention(const PagesAttnParams<kSections, kMembers> &p, const CUtensorMap &tk,
-                                   const CUtensorMap &tv, bool half, bool merge, cudaStream_t s);
+cudaError_t launch_pages_tiles(const PagesAttnParams<kSections, kMembers> &p, const PageWork &w, const CUtensorMap &tk,
+                               const CUtensorMap &tv, bool half, cudaStream_t s);
+template <int kSections, int kMembers>
+cudaError_t launch_pages_rows(const PagesAttnParams<kSections, kMembers> &p, const PageWork &w, bool half, bool beside,
+                              int sm_count, cudaStream_t s);
+template <int kSections, int kMembers>
+cudaError_t launch_pages_merge(const PagesAttnParams<kSections, kMembers> &p, bool half, cudaStream_t s);
 
 }  // namespace sdv2

@@ -42,6 +42,7 @@ class PagedKVCache:
         self.pages, self.page_tokens, self.stream_pages = pages, page_tokens, self.cfg.stream_pages
         self.max_queries, self.block_tokens = self.cfg.max_queries, block_tokens
         self.dtype = _TORCH[dtype]
+        self._views = {}
 
     def close(self):
         if self.handle:
@@ -102,8 +103,11 @@ class PagedKVCache:
 
     # -- views of the buffer (for inspection and tests)
     def _region(self, offset, dtype, *shape):
-        n = math.prod(shape) * dtype.itemsize
-        return self.buffer[offset:offset + n].view(dtype).view(*shape)
+        view = self._views.get((offset, shape))
+        if view is None:
+            n = math.prod(shape) * dtype.itemsize
+            view = self._views[offset, shape] = self.buffer[offset:offset + n].view(dtype).view(*shape)
+        return view
 
     def _pool(self, offset, layer):
         shape = (self.pages, self.kv_heads, self.page_tokens, self.head_dim)
