@@ -486,16 +486,17 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
 
     // Both parts' kernels: a warp per run where no unit has more than 16 rows.  (The groups'
     // units have at least as many rows as their streams'.)
-    const bool few_own = static_cast<int64_t>(most_tokens) * p->group <= kRowsPerWorker;
-    const bool few_common = static_cast<int64_t>(most_common) * p->group <= kRowsPerWorker;
-    auto work = [&](int begin, int end, bool few, int32_t cut_row) {
+    const int32_t own_rows = most_tokens * p->group, common_rows = most_common * p->group;
+    const bool few_own = own_rows <= kRowsPerWorker, few_common = common_rows <= kRowsPerWorker;
+    auto work = [&](int begin, int end, bool few, int32_t rows, int32_t cut_row) {
         PageWork w{};
         w.begin = begin;
         w.end = end;
         w.tile_log2 = few ? 4 : 7;
         w.tile_tokens = (few ? kRowsPerWorker : 128) / p->group;
         w.cut_row = cut_row;
-        w.cut_rows = few ? kRowsPerWorker : 128;
+        w.cut_rows = few ? rows : 128;
+        w.rows = rows;
         int64_t tiles = 0;
         for (int i = begin; i < end; ++i) {
             PageSection &x = p->section[i];
@@ -505,15 +506,16 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
             tiles += static_cast<int64_t>((x.n_tokens + w.tile_tokens - 1) / w.tile_tokens) * c.kv_heads * x.tiles;
         }
         w.tiles = static_cast<int32_t>(std::min<int64_t>(tiles, INT32_MAX));
-        const int64_t most = static_cast<int64_t>(std::min(h->sm_count, kPagesMaxCtas)) * (few ? kRowWarps : 1);
+        const int64_t ctas = std::min(h->sm_count, kPagesMaxCtas);
+        const int64_t most = few ? std::min<int64_t>(ctas * kRowWarps, kCutRows / rows) : ctas;
         const int64_t shortest = few ? 4 : 2;                // tiles of a run, at least
         w.workers = static_cast<int32_t>(std::max<int64_t>(1, std::min(most, (tiles + shortest - 1) / shortest)));
         return w;
     };
     const int32_t cut = 2 * c.max_queries * c.heads;
     const bool together = p->n_common == 0 || few_common == few_own;
-    p->own = work(together ? 0 : p->n_common, n, few_own, cut);
-    p->common = together ? p->own : work(0, p->n_common, few_common, cut + kCutRows);
+    p->own = work(together ? 0 : p->n_common, n, few_own, together ? std::max(own_rows, common_rows) : own_rows, cut);
+    p->common = together ? p->own : work(0, p->n_common, few_common, common_rows, cut + kCutRows);
     if (p->own.tiles == INT32_MAX || p->common.tiles == INT32_MAX) return fail(SDV2_E_SHAPE, "too much work for one call");
 
     const bool half = c.dtype == SDV2_DT_FP16;

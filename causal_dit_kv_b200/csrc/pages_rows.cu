@@ -6,13 +6,19 @@
 // warp, so eight runs per SM overlap their starts, ends and dependent chains (one CTA-wide
 // pipeline paid about 8000 cycles at each change of unit).
 //
-// Tensor-core products of 16 rows x 8 columns x 16 (mma.sync: the smallest tile of the
-// tcgen05 kind has 64 rows, of which these calls fill 1 to 16).  The order of the channels inside
-// q . k and of the columns of V is free, so each lane's operands are whole 16-byte pieces of
-// K and V rows: lane (g, c) = (lane / 4, lane % 4) takes channels 32 j + 8 c .. + 7 of keys g and
-// g + 8 for the scores, and channels 64 j + 8 g .. + 7 of keys 2c, 2c + 1, 2c + 8, 2c + 9 for the
-// output.  A lane copies just what it will use itself into its own slots of shared memory
-// (cp.async, no barrier, no bank conflicts), kStages tiles ahead.
+// Tensor-core products of 16 x 8 x 16 (mma.sync: the tcgen05 kind's smallest tile has 64 rows,
+// of which these calls fill 1 to 16), transposed so that keys and channels fill the 16 and the
+// query rows the 8: S^T = K Q^T, O^T = V^T P^T.  The order of the channels inside q . k and of
+// the rows of O^T is free, so each lane's operands are whole 16-byte pieces of K and V rows:
+// lane (g, c) = (lane / 4, lane % 4) takes channels 32 j + 8 c .. + 7 of keys g and g + 8 for the
+// scores, and channels 64 j + 8 g .. + 7 of keys 2c, 2c + 1, 2c + 8, 2c + 9 for the output.  P^T
+// comes from S^T by transposing 8 x 8 blocks across the lanes.
+// A tile's 16 keys are contiguous in their page; the warp copies them in 512-byte pieces (cp.async,
+// kStages tiles ahead) to rows whose 16-byte pieces are permuted by the key, so that neither the
+// copies nor both kinds of operand reads meet bank conflicts.  (Copies of just what each lane will
+// use, which would need no permutation, ran at 4.5 TB/s: they touch twice the lines.)
+//  A row's running maximum is agreed on by all its lanes only when one of
+// them sees a score over it by more than 2^8, so an ordinary tile has one vote and no reduction.
 // Keys past the range are copied as zeros and their scores masked.
 #include <algorithm>
 #include <atomic>
@@ -24,11 +30,12 @@ namespace sdv2 {
 
 template <int D>
 struct RowsLayout {
-    static constexpr int kCopies = D / 8;                 // 16-byte pieces per lane of a tile: D / 16 of K, D / 16 of V
+    static constexpr int kCopies = D / 8;                 // 512-byte pieces of a tile: D / 16 of K, D / 16 of V
+    static constexpr int kPerCopy = 256 / D;              // keys in each
     static constexpr int kTile = kCopies * 512;           // bytes of a tile
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kAlloc = kRowWarps * kStages * kTile;
-    static_assert(kAlloc <= 232448, "shared memory of one CTA");
+    static constexpr int kAlloc = kRowWarps / 2 * kStages * kTile;
+    static_assert(2 * (kAlloc + 1024) <= 233472, "two CTAs to an SM");
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t bytes) {
@@ -61,8 +68,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int D, bool HALF, int kS, int kM>
-__global__ void __launch_bounds__(kRowWarps * 32, 1)
+// An 8 x 8 block of 16-bit values, row g and columns 2c, 2c + 1 in lane (g, c), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// N: blocks of 8 query rows (1 or 2).
+template <int D, bool HALF, int N, int kS, int kM>
+__global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     pages_rows_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p, const __grid_constant__ PageWork work,
                       const bool beside) {
     using L = RowsLayout<D>;
@@ -84,182 +99,214 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1)
         pos = end = 0;
     }
     const int page_log2 = p.v.page_log2;
-    const uint32_t stage0 = smem_addr(smem) + warp * (L::kStages * L::kTile) + lane * 16;
+    // Piece x (16 bytes) of key y's row lies at place x ^ swizzle(y), swizzle(y) = (y & 6) ^ ((y & 1) << 2):
+    // lanes of one access with keys 2i, 2i + 1 and four pieces each, or with two pieces of keys 2c,
+    // take eight different places.
+    const uint32_t stage0 = smem_addr(smem) + warp * (L::kStages * L::kTile);
+    const int my_key = lane / (D / 8);                   // of a copy's kPerCopy keys
+    const uint32_t my_piece = (lane & (D / 8 - 1)) ^ (my_key & 2) ^ ((my_key & 1) << 2);
+    const uint32_t copy_to = stage0 + my_key * (D * 2);
+    const uint32_t k_place = c ^ ((g & 6) ^ ((g & 1) << 2)), v_place = g ^ (2 * c);
     for (int taken; pos < end; pos += taken) {
         const PagesRun r = pages_run(p, work, worker, pos, end, &taken);
         const PageSection &s = p.section[r.sec];
 
-        // ---- queries: rows g and g + 8 of the tile as A operands
-        uint4 q[2][D / 32];
-        int token[2], head[2], seen[2];
-        bool valid[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = g + 8 * h;
-            valid[h] = row < r.n_rows;
-            const int place = valid[h] ? row / p.group : 0;
-            head[h] = r.head * p.group + (valid[h] ? row - place * p.group : 0);
-            token[h] = query_token(p, s, place);
-            seen[h] = r.keys;                            // keys the row sees, from the range's first
-            if (!r.common) seen[h] = min(r.len, ((r.len - s.n_tokens + place) / p.block + 1) * p.block) - r.base;
-            const uint16_t *src = p.q + static_cast<int64_t>(token[h]) * p.q_stride + head[h] * D + 8 * c;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j)
-                q[h][j] = valid[h] ? *reinterpret_cast<const uint4 *>(src + 32 * j) : make_uint4(0, 0, 0, 0);
-        }
-
-        // ---- copies: page ids of the run, 32 at a time, the next 32 in flight
-        const int32_t *row_ids = p.v.table + static_cast<int64_t>(s.stream) * p.v.width + s.page0;
-        const int last_page = max(0, ((r.keys + (1 << page_log2) - 1) >> page_log2) - 1);
+        // ---- copies: page ids of the run, 32 at a time, the next 32 in flight (not waiting for the
+        // stream's length: entries behind its pages are -1)
         const int key0 = r.begin * 16;                   // first key of the run in the range
         int batch = key0 >> page_log2;
-        int ids = r.n > 0 ? row_ids[min(batch + lane, last_page)] : 0;
-        int ids_next = r.n > 0 ? row_ids[min(batch + 32 + lane, last_page)] : 0;
-        const int64_t head_off = (static_cast<int64_t>(r.head) << page_log2) * D;
+        const int32_t *row_ids = p.v.table + static_cast<int64_t>(s.stream) * p.v.width;
+        const int last_id = p.v.width - 1 - s.page0;
+        row_ids += s.page0;
+        int ids = row_ids[min(batch + lane, last_id)];
+        int ids_next = row_ids[min(batch + 32 + lane, last_id)];
         const int64_t page_elems = (static_cast<int64_t>(p.v.kv_heads) << page_log2) * D;
+        const int64_t head_off = (static_cast<int64_t>(r.head) << page_log2) * D;
+        const uint16_t *k_lane = p.k_layer + head_off + lane * 8, *v_lane = p.v_layer + head_off + lane * 8;
+        uint32_t fill = 0;                               // offset of the stage that the next copies go to
         auto issue = [&](int tile) {                     // (tiles in order)
             if (tile < r.n) {
                 const int key = key0 + tile * 16, index = key >> page_log2;
                 if (index - batch >= 32) {
                     batch += 32;
                     ids = ids_next;
-                    ids_next = row_ids[min(batch + 32 + lane, last_page)];
+                    ids_next = row_ids[min(batch + 32 + lane, last_id)];
                 }
                 int id = __shfl_sync(0xffffffffu, ids, index - batch);
                 id = min(max(id, 0), p.v.pages - 1);     // (the table lies in the caller's buffer)
-                const int64_t off = id * page_elems + head_off + static_cast<int64_t>(key & ((1 << page_log2) - 1)) * D;
+                const int64_t off = id * page_elems + (key & ((1 << page_log2) - 1)) * D;
                 const int there = r.keys - key;          // keys of the tile that there are
-                const uint32_t dst = stage0 + (tile % L::kStages) * L::kTile;
-                const uint16_t *ks = p.k_layer + off + g * D + 8 * c, *vs = p.v_layer + off + 2 * c * D + 8 * g;
+                const uint16_t *ks = k_lane + off, *vs = v_lane + off;
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int j = 0; j < D / 32; ++j)
-                        copy16(dst + (t * (D / 32) + j) * 512, ks + t * 8 * D + 32 * j, g + 8 * t < there ? 16 : 0);
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-                        copy16(dst + (D / 16 + k * (D / 64) + j) * 512, vs + ((k & 1) + (k >> 1) * 8) * D + 64 * j,
-                               2 * c + (k & 1) + (k >> 1) * 8 < there ? 16 : 0);
+                for (int k = 0; k < L::kCopies / 2; ++k) {   // keys kPerCopy k + my_key, of K and of V
+                    const uint32_t dst = copy_to + fill + k * 512 + ((my_piece ^ (L::kPerCopy * k & 6)) << 4);
+                    const uint32_t bytes = L::kPerCopy * k + my_key < there ? 16u : 0u;
+                    copy16(dst, ks + k * 256, bytes);
+                    copy16(dst + L::kTile / 2, vs + k * 256, bytes);
+                }
+                fill = fill == (L::kStages - 1) * L::kTile ? 0 : fill + L::kTile;
             }
             copies_commit();
         };
+
+        // ---- queries: row g of each block of 8 as the B operand of the scores
+        uint4 q[N][D / 32];
+#pragma unroll
+        for (int b = 0; b < N; ++b) {
+            const int row = 8 * b + g;
+            const bool there = row < r.n_rows;
+            const int place = there ? row / p.group : 0;
+            const uint16_t *src = p.q + static_cast<int64_t>(query_token(p, s, place)) * p.q_stride +
+                                  (r.head * p.group + (there ? row - place * p.group : 0)) * D + 8 * c;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+                q[b][j] = there ? *reinterpret_cast<const uint4 *>(src + 32 * j) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
         for (int i = 0; i < L::kStages - 1; ++i) issue(i);
+        // keys that rows 8 b + 2 c + x see, from the range's first; all rows see those below `all`
+        int seen[N][2];
+        int all = r.keys;
+#pragma unroll
+        for (int b = 0; b < N; ++b)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                seen[b][x] = r.keys;
+                const int row = 8 * b + 2 * c + x;
+                if (!r.common && row < r.n_rows) {
+                    const int at = r.len - s.n_tokens + row / p.group;
+                    seen[b][x] = min(r.len, (at / p.block + 1) * p.block) - r.base;
+                }
+            }
+        if (!r.common) all = min(r.len, ((r.len - s.n_tokens) / p.block + 1) * p.block) - r.base;
 
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};   // rows g, g + 8 (l: this lane's columns)
-        float o[D / 8][4];
+        float m[N][2], l[N][2];                          // running maxima (in log2 units), sums of this lane's keys
+        float o[N][D / 16][4];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j)
+        for (int b = 0; b < N; ++b) {
+            m[b][0] = m[b][1] = -INFINITY;
+            l[b][0] = l[b][1] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+            for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[b][j][i] = 0.0f;
+        }
+        uint32_t take = 0;                               // offset of the stage that holds tile `it`
         for (int it = 0; it < r.n; ++it) {
             copies_wait<L::kStages - 2>();
-            const uint32_t st = stage0 + (it % L::kStages) * L::kTile;
-            // scores of keys 0..7 and 8..15
-            float sc[2][4];
+            __syncwarp();                                // the lanes' copies are all there; the stage before is read
+            const uint32_t ks = stage0 + take + g * (D * 2), vs = stage0 + take + L::kTile / 2 + c * (4 * D);
+            take = take == (L::kStages - 1) * L::kTile ? 0 : take + L::kTile;
+            // S^T: keys g, g + 8 of rows 2c, 2c + 1; two chains, added at the end
+            float sc[N][2][4];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+            for (int b = 0; b < N; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[t][i] = 0.0f;
+                for (int i = 0; i < 4; ++i) sc[b][0][i] = sc[b][1][i] = 0.0f;
 #pragma unroll
-                for (int j = 0; j < D / 32; ++j) {
-                    const uint4 k = lds16(st + (t * (D / 32) + j) * 512);
-                    mma16816<HALF>(sc[t], q[0][j].x, q[1][j].x, q[0][j].y, q[1][j].y, k.x, k.y);
-                    mma16816<HALF>(sc[t], q[0][j].z, q[1][j].z, q[0][j].w, q[1][j].w, k.z, k.w);
+            for (int j = 0; j < D / 32; ++j) {
+                const uint32_t at = ks + (j >> 1) * 128 + ((k_place ^ (4 * (j & 1))) << 4);
+                const uint4 k0 = lds16(at), k1 = lds16(at + 8 * (D * 2));
+#pragma unroll
+                for (int b = 0; b < N; ++b) {
+                    mma16816<HALF>(sc[b][0], k0.x, k1.x, k0.y, k1.y, q[b][j].x, q[b][j].y);
+                    mma16816<HALF>(sc[b][1], k0.z, k1.z, k0.w, k1.w, q[b][j].z, q[b][j].w);
                 }
             }
-            const int first = key0 + it * 16 + 2 * c;    // key of sc[0][0]
-            uint32_t pk[2][2];                           // P, [keys 0..7, 8..15][row g, g + 8]
+            uint32_t pt[N][2];                           // P^T: keys 2c, 2c + 1 (and + 8) of row g
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int b = 0; b < N; ++b) {
+                float x[4];                              // [key g, g + 8][row 2c, 2c + 1]
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int i = 0; i < 4; ++i) x[i] = (sc[b][0][i] + sc[b][1][i]) * p.scale_log2;
+                if (key0 + it * 16 + 16 > all) {         // a key here is not every row's
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + it * 16 + g + 8 * (i >> 1) >= seen[b][i & 1]) x[i] = -INFINITY;
+                }
+                const float m0 = fmaxf(x[0], x[2]), m1 = fmaxf(x[1], x[3]);
+                if (__any_sync(0xffffffffu, m0 > m[b][0] + kCoreRescale || m1 > m[b][1] + kCoreRescale)) {
+                    float t[2] = {m0, m1};
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        float &x = sc[t][2 * h + i];
-                        x = first + 8 * t + i < seen[h] ? x * p.scale_log2 : -INFINITY;
-                    }
-                float mt = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-                // the running maximum moves only when a tile exceeds it by more than 2^8
-                const bool up = mt > m[h] + kCoreRescale || m[h] == -INFINITY;
-                if (__any_sync(0xffffffffu, up && it > 0)) {
-                    const float alpha = !up ? 1.0f : (m[h] == -INFINITY ? 0.0f : ex2_approx(m[h] - mt));
-                    l[h] *= alpha;
 #pragma unroll
-                    for (int j = 0; j < D / 8; ++j) {
-                        o[j][2 * h] *= alpha;
-                        o[j][2 * h + 1] *= alpha;
+                        for (int d = 4; d < 32; d <<= 1) t[i] = fmaxf(t[i], __shfl_xor_sync(0xffffffffu, t[i], d));
+                        t[i] = fmaxf(t[i], m[b][i]);
+                        const float alpha = m[b][i] == -INFINITY ? 0.0f : ex2_approx(m[b][i] - t[i]);
+                        m[b][i] = t[i];
+                        l[b][i] *= alpha;
+#pragma unroll
+                        for (int j = 0; j < D / 16; ++j) {
+                            o[b][j][i] *= alpha;
+                            o[b][j][2 + i] *= alpha;
+                        }
                     }
                 }
-                if (up) m[h] = mt;
-                const float ref = m[h] == -INFINITY ? 0.0f : m[h];
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const float p0 = ex2_approx(sc[t][2 * h] - ref), p1 = ex2_approx(sc[t][2 * h + 1] - ref);
-                    l[h] += p0 + p1;
-                    pk[t][h] = pack_16x2<HALF>(p0, p1);
-                }
+                const float r0 = m[b][0] == -INFINITY ? 0.0f : m[b][0], r1 = m[b][1] == -INFINITY ? 0.0f : m[b][1];
+                const float p0 = ex2_approx(x[0] - r0), p1 = ex2_approx(x[1] - r1);
+                const float p2 = ex2_approx(x[2] - r0), p3 = ex2_approx(x[3] - r1);
+                l[b][0] += p0 + p2;
+                l[b][1] += p1 + p3;
+                pt[b][0] = transpose8(pack_16x2<HALF>(p0, p1));
+                pt[b][1] = transpose8(pack_16x2<HALF>(p2, p3));
             }
-            // output: V of keys 2c, 2c + 1 and 2c + 8, 2c + 9, pairs of keys packed per channel
+            // O^T: V of keys 2c, 2c + 1 and 2c + 8, 2c + 9, pairs of keys packed per channel
 #pragma unroll
             for (int j = 0; j < D / 64; ++j) {
                 uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = lds16(st + (D / 16 + k * (D / 64) + j) * 512);
+                for (int k = 0; k < 4; ++k)             // keys 2c + (k & 1) + 8 (k / 2)
+                    v[k] = lds16(vs + ((k & 1) + 8 * (k >> 1)) * (D * 2) + j * 128 + ((v_place ^ (4 * (k & 1))) << 4));
                 const uint32_t *a = &v[0].x, *b = &v[1].x, *e = &v[2].x, *f = &v[3].x;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mma16816<HALF>(o[8 * j + 2 * i], pk[0][0], pk[0][1], pk[1][0], pk[1][1],
-                                   __byte_perm(a[i], b[i], 0x5410), __byte_perm(e[i], f[i], 0x5410));
-                    mma16816<HALF>(o[8 * j + 2 * i + 1], pk[0][0], pk[0][1], pk[1][0], pk[1][1],
-                                   __byte_perm(a[i], b[i], 0x7632), __byte_perm(e[i], f[i], 0x7632));
+                    const uint32_t a0 = __byte_perm(a[i], b[i], 0x5410), a1 = __byte_perm(a[i], b[i], 0x7632);
+                    const uint32_t a2 = __byte_perm(e[i], f[i], 0x5410), a3 = __byte_perm(e[i], f[i], 0x7632);
+#pragma unroll
+                    for (int n = 0; n < N; ++n) mma16816<HALF>(o[n][4 * j + i], a0, a1, a2, a3, pt[n][0], pt[n][1]);
                 }
             }
             issue(it + L::kStages - 1);
         }
         copies_wait<0>();
 
-        // ---- results: o[8 j + i][2 h + x] is channel 64 j + 16 c + 8 x + i of row g + 8 h
+        // ---- results: o[b][4 j + i][2 y + x] is channel 64 j + 8 g + 2 i + y of row 8 b + 2 c + x
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (!valid[h]) continue;
-            if (r.whole && !r.common && s.common < 0) {
-                const float inv = 1.0f / l[h];
-                uint16_t *orow = p.out + static_cast<int64_t>(token[h]) * p.out_stride + head[h] * D + 16 * c;
+        for (int b = 0; b < N; ++b)
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j)
+            for (int x = 0; x < 2; ++x) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                for (int d = 4; d < 32; d <<= 1) l[b][x] += __shfl_xor_sync(0xffffffffu, l[b][x], d);
+                const int row = 8 * b + 2 * c + x;
+                if (row >= r.n_rows) continue;
+                const int place = row / p.group, head = r.head * p.group + row - place * p.group;
+                const int token = query_token(p, s, place);
+                if (r.whole && !r.common && s.common < 0) {
+                    const float inv = 1.0f / l[b][x];
+                    uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + 8 * g;
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j) {
                         uint32_t y[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            y[i] = pack_16x2<HALF>(o[8 * j + 2 * i][2 * h + x] * inv, o[8 * j + 2 * i + 1][2 * h + x] * inv);
-                        *reinterpret_cast<uint4 *>(orow + 64 * j + 8 * x) = make_uint4(y[0], y[1], y[2], y[3]);
+                            y[i] = pack_16x2<HALF>(o[b][4 * j + i][x] * inv, o[b][4 * j + i][2 + x] * inv);
+                        *reinterpret_cast<uint4 *>(orow + 64 * j) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-            } else {
-                const int64_t part = partial_row(p, work, r, worker, g + 8 * h,
-                                                 static_cast<int64_t>(token[h]) * p.heads + head[h]);
-                if (r.n > 0) {
-                    float *prow = p.part_o + part * D + 16 * c;
+                } else {
+                    const int64_t part = partial_row(p, work, r, worker, row, static_cast<int64_t>(token) * p.heads + head);
+                    if (r.n > 0) {
+                        float *prow = p.part_o + part * D + 8 * g;
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
+                        for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-#pragma unroll
-                            for (int i = 0; i < 8; i += 4)
-                                *reinterpret_cast<float4 *>(prow + 64 * j + 8 * x + i) =
-                                    make_float4(o[8 * j + i][2 * h + x], o[8 * j + i + 1][2 * h + x],
-                                                o[8 * j + i + 2][2 * h + x], o[8 * j + i + 3][2 * h + x]);
+                            for (int i = 0; i < 4; i += 2)
+                                *reinterpret_cast<float4 *>(prow + 64 * j + 2 * i) =
+                                    make_float4(o[b][4 * j + i][x], o[b][4 * j + i][2 + x], o[b][4 * j + i + 1][x],
+                                                o[b][4 * j + i + 1][2 + x]);
+                    }
+                    if (g == 0) p.part_ml[part] = make_float2(m[b][x], l[b][x]);
                 }
-                if (c == 0) p.part_ml[part] = make_float2(m[h], l[h]);
             }
-        }
     }
     if (beside) grid_dependency_wait();
 }
@@ -363,8 +410,8 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
         *reinterpret_cast<uint32_t *>(orow) = pack_16x2<HALF>(acc[0] * inv, acc[1] * inv);
 }
 
-template <int D, bool HALF, int kS, int kM>
-static cudaError_t launch_rows_d(const PagesAttnParams<kS, kM> &p, const PageWork &w, bool beside, int sm_count,
+template <int D, bool HALF, int N, int kS, int kM>
+static cudaError_t launch_rows_n(const PagesAttnParams<kS, kM> &p, const PageWork &w, bool beside, int sm_count,
                                  cudaStream_t s) {
     static std::atomic<uint64_t> configured{0};          // (per device)
     int dev = 0;
@@ -372,15 +419,23 @@ static cudaError_t launch_rows_d(const PagesAttnParams<kS, kM> &p, const PageWor
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
-        e = cudaFuncSetAttribute(pages_rows_kernel<D, HALF, kS, kM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(pages_rows_kernel<D, HALF, N, kS, kM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  RowsLayout<D>::kAlloc);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    // few workers: fewer warps to a CTA, over all the SMs
-    const int warps = std::min(kRowWarps, (w.workers + sm_count - 1) / sm_count);
-    return launch_dependent(pages_rows_kernel<D, HALF, kS, kM>, dim3((w.workers + warps - 1) / warps), dim3(warps * 32),
+    // four warps to a CTA, two CTAs to an SM (a batch of 604 MB: 101 us, with 2 warps 121, with 8
+    // 102); few workers are spread over all SMs
+    const int warps = std::min(kRowWarps / 2, (w.workers + sm_count - 1) / sm_count);
+    return launch_dependent(pages_rows_kernel<D, HALF, N, kS, kM>, dim3((w.workers + warps - 1) / warps), dim3(warps * 32),
                             static_cast<size_t>(warps * RowsLayout<D>::kStages * RowsLayout<D>::kTile), s, p, w, beside);
+}
+
+template <int D, bool HALF, int kS, int kM>
+static cudaError_t launch_rows_d(const PagesAttnParams<kS, kM> &p, const PageWork &w, bool beside, int sm_count,
+                                 cudaStream_t s) {
+    return w.rows <= 8 ? launch_rows_n<D, HALF, 1>(p, w, beside, sm_count, s)
+                       : launch_rows_n<D, HALF, 2>(p, w, beside, sm_count, s);
 }
 
 template <int kS, int kM>

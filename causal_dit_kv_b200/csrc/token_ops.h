@@ -34,7 +34,7 @@ cudaError_t prompt_status(uint32_t *word);
 // ---------------------------------------------------------------- paged cache
 constexpr int kPagesMaxStreams = 256;
 constexpr int kPagesMaxCtas = 160;        // attention CTAs of one launch, at most (scratch is sized for them)
-constexpr int kRowWarps = 8;              // warps of a CTA of the few-row kernel, each a worker of its own
+constexpr int kRowWarps = 8;              // warps of an SM in the few-row kernel, each a worker of its own
 constexpr int kRowsPerWorker = 16;        // query rows that one of them takes, at most
 
 // Status bits of the paged cache's word besides the waits of sdv2_internal.h.
@@ -106,6 +106,7 @@ struct PageSection {
 // rows at partial row cut_row + worker * cut_rows.
 struct PageWork {
     int32_t begin, end, tiles, workers, tile_log2, tile_tokens, cut_row, cut_rows;
+    int32_t rows;                         // most query rows of a unit
 };
 
 template <int kSections, int kMembers>
