@@ -14,7 +14,10 @@
 //   warps 4..7  softmax and epilogue of query tile 0 (a thread per row), 8..11 of tile 1
 // TMEM: S_0 | S_1 | O_0 | O_1 (128 columns each); P_t, 16-bit, over the first half of S_t.
 // While one tile is in the softmax the tensor core works on the other.
-// Units are taken longest first, so the launch does not end on a long one.
+// Units are taken longest first, so the launch does not end on a long one.  The grid has one
+// CTA per unit; each running CTA (one per SM) takes further units over from CTAs that have not
+// started (clusterlaunchcontrol), so its set-up is paid once, the next unit's first tiles and
+// scores are under way while the last one's results are written, and SMs that run faster take more.
 // Every wait is bounded; a wait that runs out records itself in g_prompt_status.
 #include <atomic>
 
@@ -39,8 +42,12 @@ struct PromptLayout {
     static constexpr int kKFull = 2, kKEmpty = kKFull + kKStages;
     static constexpr int kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages;
     static constexpr int kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kOFull = kPFull + 2;
-    static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1, kNumBars = kDrain + 1;
-    static constexpr int kMisc = kBar + kNumBars * 8;     // TMEM base, abort flag
+    static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1;
+    // units: the current one is near its end, answer to a request landed, unit number published in a
+    // slot, slot read by every role
+    static constexpr int kNear = kDrain + 1, kAnswer = kNear + 1, kUnitFull = kAnswer + 1, kUnitEmpty = kUnitFull + 2, kNumBars = kUnitEmpty + 2;
+    static constexpr int kUnits = kBar + ((kNumBars * 8 + 15) & ~15);   // the answer (16 bytes), two unit slots
+    static constexpr int kMisc = kUnits + 32;             // TMEM base, abort flag
     static constexpr int kAlloc = kMisc + 16 + 1024;      // room to align the base to 1024 bytes
     static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
@@ -81,6 +88,52 @@ __device__ __forceinline__ int tail_rows(const PromptUnit &w) {
     return left < 128 ? left : 0;
 }
 
+// Ask for the next CTA that has not started; the 16-byte answer lands at `answer`, counted on `bar`.
+__device__ __forceinline__ void request_cta(void *answer, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_addr(answer)),
+        "r"(smem_addr(bar))
+        : "memory");
+}
+
+// The CTA number in an answer, or -1 if none was left.
+__device__ __forceinline__ int answered_cta(const void *answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_addr(answer))
+        : "memory");
+    return got ? static_cast<int>(x) : -1;
+}
+
+// A role's view of the CTA's units, in order.  The first is the CTA's own; later ones are
+// published by warp 3 in two slots.  Every role's thread (or warp, converged) calls next().
+struct UnitFeed {
+    uint64_t *full, *empty;
+    volatile int *slot;
+    int n = 0;
+    // The next unit, or -1 at the end or when a wait ran out.  whole_warp: all lanes call it.
+    __device__ __forceinline__ int next(bool whole_warp, int lane, volatile uint32_t *abort, uint32_t *status) {
+        if (n++ == 0) return blockIdx.x;
+        const int x = n & 1, round = ((n - 2) >> 1) & 1;
+        bool ok = mbar_wait(&full[x], round, abort, status, kStatusTmaWait);
+        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return -1;
+        const int u = slot[x];
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(&empty[x]);
+        return u;
+    }
+};
+constexpr int kUnitReaders = 11;          // producer, MMA issuer, warp 2, eight softmax warps
+
 template <int D, bool HALF, int kItems>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     prompt_attention_kernel(const __grid_constant__ PromptParams<kItems> p, const __grid_constant__ CUtensorMap tmap_q,
@@ -95,7 +148,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int b = 0; b < L::kNumBars; ++b) mbar_init(&bars[b], b == L::kPFull || b == L::kPFull + 1 ? 128 : 1);
+        for (int b = 0; b < L::kNumBars; ++b)
+            mbar_init(&bars[b], b == L::kPFull || b == L::kPFull + 1 ? 128 : (b >= L::kUnitEmpty ? kUnitReaders : 1));
         *abort_flag = 0u;
         fence_barrier_init();
         tma_prefetch_desc(&tmap_q);
@@ -114,13 +168,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     grid_dependency_wait();                     // the inputs may come from the kernel just before
     grid_launch_dependents();
 
+    UnitFeed feed;
+    feed.full = &bars[L::kUnitFull];
+    feed.empty = &bars[L::kUnitEmpty];
+    feed.slot = reinterpret_cast<volatile int *>(smem + L::kUnits + 16);
+
     if (warp < 4) {
         regs_dec<80>();
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             int kc = 0, vc = 0, uc = 0;         // K tiles, V tiles and units issued so far
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x, ++uc) {
+            for (int u; ok && (u = feed.next(false, lane, abort_flag, status)) >= 0; ++uc) {
                 const PromptUnit w = prompt_unit(p, u);
                 ok = mbar_wait(&bars[L::kQEmpty], (uc & 1) ^ 1, abort_flag, status, kStatusTmaWait);
                 if (!ok) break;
@@ -190,7 +249,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             int kc = 0, vc = 0, uc = 0, fixes = 0, pc[2] = {0, 0};
             bool ok = true;
-            for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x, ++uc) {
+            for (int u; ok && (u = feed.next(false, lane, abort_flag, status)) >= 0; ++uc) {
                 const PromptUnit w = prompt_unit(p, u);
                 ok = mbar_wait(&bars[L::kQFull], uc & 1, abort_flag, status, kStatusMmaWait) &&
                      mbar_wait(&bars[L::kKFull + kc % L::kKStages], (kc / L::kKStages) & 1, abort_flag, status,
@@ -205,6 +264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (w.n_max == 1) umma_commit(&bars[L::kQEmpty]);
                 const bool tail = tail_rows(w) > 0;
                 for (int it = 0; ok && it < w.n_max; ++it) {
+                    if (it == max(0, w.n_max - 3)) mbar_arrive(&bars[L::kNear]);
                     const int st = vc % L::kVStages;
                     ok = mbar_wait(&bars[L::kVFull + st], (vc / L::kVStages) & 1, abort_flag, status, kStatusMmaWait);
                     if (ok && tail && it == w.n_max - 1) {
@@ -258,7 +318,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // ------------------------------------------------ ends of sequences in V
             // (asked by the MMA issuer: a parity wait on the ring itself could be passed by)
             int vc = 0, fixes = 0;
-            for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
+            for (int u; (u = feed.next(true, lane, abort_flag, status)) >= 0;) {
                 const PromptUnit w = prompt_unit(p, u);
                 vc += w.n_max;
                 const int valid = tail_rows(w);
@@ -267,6 +327,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 ++fixes;
                 zero_tail_rows<D>(smem + L::kV + (vc - 1) % L::kVStages * L::kTile, valid, lane);
                 if (lane == 0) mbar_arrive(&bars[L::kVFix]);
+            }
+        } else if (warp == 3 && lane == 0) {
+            // ------------------------------------------------ further units
+            // (one request at a time, when the current unit is near its end: asked for earlier, long units
+            // would pile up on the CTAs that began with long ones; none after the first that finds no
+            // CTA left)
+            volatile int *slot = feed.slot;
+            for (int i = 0, u = 0; u >= 0; ++i) {
+                const int x = i & 1;
+                if (!mbar_wait(&bars[L::kNear], i & 1, abort_flag, status, kStatusTmaWait)) break;
+                mbar_arrive_expect_tx(&bars[L::kAnswer], 16);
+                request_cta(smem + L::kUnits, &bars[L::kAnswer]);
+                u = mbar_wait(&bars[L::kAnswer], i & 1, abort_flag, status, kStatusTmaWait)
+                        ? answered_cta(smem + L::kUnits)
+                        : -1;
+                fence_proxy_async_shared();      // the answer has been read before the next one is written
+                if (!mbar_wait(&bars[L::kUnitEmpty + x], ((i >> 1) & 1) ^ 1, abort_flag, status, kStatusTmaWait)) break;
+                slot[x] = u;
+                mbar_arrive(&bars[L::kUnitFull + x]);
             }
         }
     } else {
@@ -278,7 +357,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
         int sc = 0, oc = 0;                          // score tiles and accumulators seen so far
         bool ok = true;
-        for (int u = blockIdx.x; ok && u < p.n_units; u += gridDim.x) {
+        for (int u; ok && (u = feed.next(true, lane, abort_flag, status)) >= 0;) {
             const PromptUnit w = prompt_unit(p, u);
             const int n = t ? w.n[1] : w.n[0];
             if (n == 0) continue;
