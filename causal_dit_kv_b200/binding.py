@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdv2.so")
@@ -104,18 +105,18 @@ _SIGNATURES = [
     ("sdv2_attention_pair_mode", c_int32, [POINTER(sdv2_cache_config), POINTER(c_int64), c_int32]),
     ("sdv2_append_attention_mode", c_int32, [POINTER(sdv2_cache_config), POINTER(c_int64), c_int32]),
     ("sdv2_prompt_attention", c_int32, [POINTER(sdv2_prompt_config), c_void_p, c_void_p, c_void_p, c_void_p,
-                                        POINTER(c_int64), c_int32, c_float, c_void_p]),
+                                        c_void_p, c_int32, c_float, c_void_p]),
     ("sdv2_prompt_check", c_int32, []),
     ("sdv2_pages_bytes", c_size_t, [POINTER(sdv2_pages_config)]),
     ("sdv2_pages_layout_of", c_int32, [POINTER(sdv2_pages_config), POINTER(sdv2_pages_layout)]),
     ("sdv2_pages_create", c_int32, [POINTER(sdv2_pages_config), c_void_p, c_size_t, POINTER(c_void_p)]),
     ("sdv2_pages_destroy", c_int32, [c_void_p]),
-    ("sdv2_pages_extend", c_int32, [c_void_p, POINTER(c_int32), c_void_p]),
-    ("sdv2_pages_write", c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, POINTER(c_int32), c_void_p]),
+    ("sdv2_pages_extend", c_int32, [c_void_p, c_void_p, c_void_p]),
+    ("sdv2_pages_write", c_int32, [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_void_p]),
     ("sdv2_pages_attention", c_int32,
-     [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, POINTER(c_int32), c_float, c_void_p]),
-    ("sdv2_pages_fork", c_int32, [c_void_p, c_int32, POINTER(c_int32), c_int32, c_int32, c_void_p]),
-    ("sdv2_pages_free", c_int32, [c_void_p, POINTER(c_int32), c_int32, c_void_p]),
+     [c_void_p, c_int32, c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_float, c_void_p]),
+    ("sdv2_pages_fork", c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p]),
+    ("sdv2_pages_free", c_int32, [c_void_p, c_void_p, c_int32, c_void_p]),
     ("sdv2_pages_compact", c_int32, [c_void_p, POINTER(c_int32), c_void_p]),
     ("sdv2_pages_query", c_int32,
      [c_void_p, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, POINTER(c_int32), POINTER(c_int32)]),
@@ -163,10 +164,31 @@ def _ptr(x):
     raise TypeError(f"cannot pass {type(x)} as a device pointer")
 
 
+_current = None
+
+
+def _current_calls():
+    """torch's own calls behind torch.cuda.current_device() and current_stream(): the index and the raw
+    stream, without the objects around them (about 4 us a call)."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.init()
+        try:
+            _current = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+        except AttributeError:
+            _current = (torch.cuda.current_device, lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _current
+
+
+def current_device() -> int:
+    return (_current or _current_calls())[0]()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        device, stream = _current or _current_calls()
+        return stream(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -349,11 +371,12 @@ def sdv2_attention_plan(cfg: sdv2_cache_config, keys, sm_count: int):
 
 def sdv2_prompt_attention(cfg: sdv2_prompt_config, q, k, v, out, offsets, softmax_scale: float, stream=None) -> None:
     """q, k, v, out: device pointers (or contiguous device tensors); offsets: n_seqs + 1 host integers."""
-    n = len(offsets)
+    arr = array("q", offsets)
+    n = len(arr)
     if n < 1:
         raise ValueError("offsets needs at least one entry")
-    _check(lib().sdv2_prompt_attention(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(out), (c_int64 * n)(*offsets),
-                                       n - 1, float(softmax_scale), _stream(stream)), "sdv2_prompt_attention")
+    _check(lib().sdv2_prompt_attention(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _address(arr), n - 1,
+                                       softmax_scale, _stream(stream)), "sdv2_prompt_attention")
 
 
 def sdv2_prompt_check() -> int:
@@ -374,10 +397,12 @@ def make_pages_config(streams, layers, heads, kv_heads, head_dim, pages, page_to
 
 
 def int32_array(values):
-    """A ctypes int32 array of host integers."""
-    if isinstance(values, ctypes.Array):
-        return values
-    return (c_int32 * len(values))(*values)
+    """Host integers as int32 values in memory."""
+    return values if isinstance(values, array) else array("i", values)
+
+
+def _address(values):
+    return values.buffer_info()[0]
 
 
 def sdv2_pages_bytes(cfg: sdv2_pages_config) -> int:
@@ -405,27 +430,32 @@ def sdv2_pages_destroy(pages: int) -> None:
 
 def sdv2_pages_extend(pages: int, counts, stream=None) -> None:
     """counts: one host integer per stream (as for every call with counts)."""
-    _check(lib().sdv2_pages_extend(pages, int32_array(counts), _stream(stream)), "sdv2_pages_extend")
+    arr = int32_array(counts)
+    _check(lib().sdv2_pages_extend(pages, _address(arr), _stream(stream)), "sdv2_pages_extend")
 
 
 def sdv2_pages_write(pages: int, layer: int, k, v, k_stride: int, v_stride: int, counts, stream=None) -> None:
-    _check(lib().sdv2_pages_write(pages, layer, _ptr(k), _ptr(v), k_stride, v_stride, int32_array(counts),
-                                  _stream(stream)), "sdv2_pages_write")
+    arr = int32_array(counts)
+    _check(lib().sdv2_pages_write(pages, layer, _ptr(k), _ptr(v), k_stride, v_stride, _address(arr), _stream(stream)),
+           "sdv2_pages_write")
 
 
 def sdv2_pages_attention(pages: int, layer: int, q, out, q_stride: int, out_stride: int, counts, softmax_scale: float,
                          stream=None) -> None:
-    _check(lib().sdv2_pages_attention(pages, layer, _ptr(q), _ptr(out), q_stride, out_stride, int32_array(counts),
-                                      float(softmax_scale), _stream(stream)), "sdv2_pages_attention")
+    arr = int32_array(counts)
+    _check(lib().sdv2_pages_attention(pages, layer, _ptr(q), _ptr(out), q_stride, out_stride, _address(arr),
+                                      softmax_scale, _stream(stream)), "sdv2_pages_attention")
 
 
 def sdv2_pages_fork(pages: int, src: int, dst, deep: bool = False, stream=None) -> None:
-    _check(lib().sdv2_pages_fork(pages, src, int32_array(dst), len(dst), 1 if deep else 0, _stream(stream)),
+    arr = int32_array(dst)
+    _check(lib().sdv2_pages_fork(pages, src, _address(arr), len(arr), 1 if deep else 0, _stream(stream)),
            "sdv2_pages_fork")
 
 
 def sdv2_pages_free(pages: int, streams, stream=None) -> None:
-    _check(lib().sdv2_pages_free(pages, int32_array(streams), len(streams), _stream(stream)), "sdv2_pages_free")
+    arr = int32_array(streams)
+    _check(lib().sdv2_pages_free(pages, _address(arr), len(arr), _stream(stream)), "sdv2_pages_free")
 
 
 def sdv2_pages_compact(pages: int, stream=None) -> int:

@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     feed.slot = reinterpret_cast<volatile int *>(smem + L::kUnits + 16);
 
     if (warp < 4) {
-        regs_dec<80>();
+        regs_dec<120>();                         // (104: 197 us for five ragged prompts, 80, where the issuer spills: 207; 120: 193)
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer
             int kc = 0, vc = 0, uc = 0;         // K tiles, V tiles and units issued so far
@@ -273,7 +273,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         ++fixes;
                     }
                     if (!ok) break;
-                    bool next_k = false;        // K tile it + 1 has landed
+                    const bool next_k = it + 1 < w.n_max;   // (waited for here, not between the products)
+                    if (next_k)
+                        ok = mbar_wait(&bars[L::kKFull + kc % L::kKStages], (kc / L::kKStages) & 1, abort_flag, status,
+                                       kStatusMmaWait);
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (!ok || it >= w.n[t]) continue;
@@ -283,13 +286,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         tc_fence_after();
                         issue_pv(t, st, it > 0);
                         if (it + 1 < w.n[t]) {
-                            if (!next_k) {
-                                ok = mbar_wait(&bars[L::kKFull + kc % L::kKStages], (kc / L::kKStages) & 1, abort_flag,
-                                               status, kStatusMmaWait);
-                                if (!ok) continue;
-                                next_k = true;
-                                tc_fence_after();
-                            }
                             issue_qk(t, kc % L::kKStages);
                         } else {
                             umma_commit(&bars[L::kOFull + t]);
@@ -350,7 +346,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     } else {
         // ------------------------------------------------ softmax and epilogue
-        regs_inc<208>();
+        regs_inc<192>();
         const int t = (warp - 4) >> 2;
         const int row = ((warp & 3) << 5) + lane;    // TMEM lane == row of the query tile
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) << 5) << 16;

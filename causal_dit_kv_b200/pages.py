@@ -33,9 +33,9 @@ class PagedKVCache:
         self.nbytes = B.sdv2_pages_bytes(self.cfg)
         self.handle = None
         self.buffer = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        if self.buffer.device.index != torch.cuda.current_device():
+        if self.buffer.get_device() < 0 or self.buffer.get_device() != B.current_device():
             raise ValueError(f"{self.buffer.device} is not the current device")
-        self.device = self.buffer.device
+        self.device = self.buffer.get_device()
         self.handle = B.sdv2_pages_create(self.cfg, self.buffer, self.nbytes)
         self.layout = B.sdv2_pages_layout_get(self.handle)
         self.streams, self.layers, self.heads, self.kv_heads, self.head_dim = streams, layers, heads, kv_heads, head_dim
@@ -61,9 +61,9 @@ class PagedKVCache:
         return B.int32_array(counts)
 
     def _rows(self, x, name, heads, n):
-        ptr, stride = rows_3d(x, name, heads, self.head_dim, self.dtype, self.device)
-        if x.shape[0] != n:
-            raise ValueError(f"{name} has {x.shape[0]} tokens, counts say {n}")
+        ptr, stride, tokens = rows_3d(x, name, heads, self.head_dim, self.dtype, self.device)
+        if tokens != n:
+            raise ValueError(f"{name} has {tokens} tokens, counts say {n}")
         return ptr, stride
 
     # -- streams and pages

@@ -75,7 +75,7 @@ def test_pages_layout(B):
 
 def test_pages_null_handles(B):
     lib = B.lib()
-    one = B.int32_array([0])
+    one = B.int32_array([0]).buffer_info()[0]
     assert lib.sdv2_pages_extend(None, one, None) == B.SDV2_E_ARG
     assert lib.sdv2_pages_write(None, 0, 16, 16, 0, 0, one, None) == B.SDV2_E_ARG
     assert lib.sdv2_pages_attention(None, 0, 16, 16, 0, 0, one, 1.0, None) == B.SDV2_E_ARG
