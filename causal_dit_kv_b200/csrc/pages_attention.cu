@@ -14,8 +14,10 @@
 //   warp 0      looks up pages, one TMA box per page and 64 channels (a lane each)
 //   warp 1      MMA issuer: tile i of a run goes to accumulator set i & 1
 //   warp 2      zeroes the rows of a run's last V tile behind its keys
+//   warp 3      works out the CTA's runs, one ahead of the others
 //   warps 4..7  softmax of set 0, 8..11 of set 1 (thread = query row); both gather the
-//               queries into shared memory and merge the two sets at the end
+//               queries into shared memory (read from memory while the run before is written
+//               out) and merge the two sets at the end
 // A query tile holds the rows (token, head of the group); rows beyond them cost no
 // exponentials.
 #include <atomic>
@@ -39,8 +41,10 @@ struct PagesLayout {
     static constexpr int kKFull = 1, kKEmpty = kKFull + kStages;
     static constexpr int kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages;
     static constexpr int kSFull = kVEmpty + kStages, kPFull = kSFull + 2, kOFull = kPFull + 2;
-    static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1, kNumBars = kDrain + 1;
-    static constexpr int kMisc = kBar + kNumBars * 8;
+    static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1;
+    static constexpr int kRunFull = kDrain + 1, kRunEmpty = kRunFull + 2, kNumBars = kRunEmpty + 2;
+    static constexpr int kRuns = kBar + kNumBars * 8;     // two slots for the CTA's next runs
+    static constexpr int kMisc = kRuns + 2 * static_cast<int>(sizeof(PagesRun));
     static constexpr int kAlloc = kMisc + 16 + 1024;
     static_assert(kAlloc <= 232448, "shared memory of one CTA");
 };
@@ -50,6 +54,27 @@ __device__ __forceinline__ int tail_keys(const PagesRun &r) {
     const int left = r.keys - (r.begin + r.n - 1) * 128;
     return r.n > 0 && left < 128 ? left : 0;
 }
+
+// A role's view of the CTA's runs, published by warp 3 in two slots.  Every role's thread (or warp,
+// converged) calls next().
+struct RunFeed {
+    uint64_t *full, *empty;
+    const PagesRun *slot;
+    int n = 0;
+    // The next run; false at the end or when a wait ran out.  whole_warp: all lanes call it.
+    __device__ __forceinline__ bool next(PagesRun *r, bool whole_warp, int lane, volatile uint32_t *abort, uint32_t *status) {
+        const int x = n & 1, round = (n >> 1) & 1;
+        ++n;
+        bool ok = mbar_wait(&full[x], round, abort, status, kStatusTmaWait);
+        if (whole_warp) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        *r = slot[x];
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(&empty[x]);
+        return r->n >= 0;
+    }
+};
+constexpr int kRunReaders = 11;           // producer, MMA issuer, warp 2, eight softmax warps
 
 template <int D, bool HALF, int kS, int kM>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -66,7 +91,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < L::kNumBars; ++b)
-            mbar_init(&bars[b], b == L::kQReady ? 256 : (b == L::kPFull || b == L::kPFull + 1 ? 128 : 1));
+            mbar_init(&bars[b], b == L::kQReady ? 256
+                                : b == L::kPFull || b == L::kPFull + 1 ? 128
+                                : b >= L::kRunEmpty ? kRunReaders : 1);
         *abort_flag = 0u;
         fence_barrier_init();
         tma_prefetch_desc(&tmap_k);
@@ -84,13 +111,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     grid_dependency_wait();                     // queries, pages and tables may come from the kernels before
     grid_launch_dependents();
 
-    // this CTA's tiles (none if the tables are not those of the call)
-    int pos0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * work.tiles / work.workers);
-    int end = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * work.tiles / work.workers);
-    if (*p.v.version != p.v.expect) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(status, kStatusStale);
-        end = pos0 = 0;
-    }
+    RunFeed feed;
+    feed.full = &bars[L::kRunFull];
+    feed.empty = &bars[L::kRunEmpty];
+    feed.slot = reinterpret_cast<const PagesRun *>(smem + L::kRuns);
     const int page_log2 = p.v.page_log2;
 
     if (warp < 4) {
@@ -102,8 +126,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t box_bytes = 128u << page_log2;
             int kc = 0, vc = 0;
             bool ok = true;
-            for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
+            for (PagesRun r; ok && feed.next(&r, true, lane, abort_flag, status);) {
                 if (r.n == 0) continue;
                 const PageSection &s = p.section[r.sec];
                 const int32_t *row = p.v.table + static_cast<int64_t>(s.stream) * p.v.width + s.page0;
@@ -191,8 +214,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 ++kc;
                 return true;
             };
-            for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
+            for (PagesRun r; ok && feed.next(&r, false, lane, abort_flag, status);) {
                 if (r.n == 0) continue;
                 ok = mbar_wait(&bars[L::kQReady], runs & 1, abort_flag, status, kStatusMmaWait);
                 ++runs;
@@ -237,8 +259,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         } else if (warp == 2) {
             // ------------------------------------------------ ends of key ranges in V
             int vc = 0, fixes = 0;
-            for (int pos = pos0, taken; pos < end; pos += taken) {
-                const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
+            for (PagesRun r; feed.next(&r, true, lane, abort_flag, status);) {
                 vc += r.n;
                 const int valid = tail_keys(r);
                 if (valid == 0) continue;
@@ -246,6 +267,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 ++fixes;
                 zero_tail_rows<D>(smem + L::kV + (vc - 1) % L::kStages * L::kTile, valid, lane);
                 if (lane == 0) mbar_arrive(&bars[L::kVFix]);
+            }
+        } else if (warp == 3 && lane == 0) {
+            // ------------------------------------------------ the CTA's runs
+            int pos = static_cast<int>(first_place(work, blockIdx.x));
+            int end = static_cast<int>(first_place(work, blockIdx.x + 1));
+            if (*p.v.version != p.v.expect) {    // (none: the tables are not those of the call)
+                if (blockIdx.x == 0) atomicOr(status, kStatusStale);
+                end = pos;
+            }
+            PagesRun *slot = reinterpret_cast<PagesRun *>(smem + L::kRuns);
+            PagesRun r;
+            r.n = 0;
+            for (int i = 0; r.n >= 0; ++i) {
+                const int x = i & 1;
+                if (!next_run(p, work, blockIdx.x, &pos, end, &r)) r.n = -1;
+                if (!mbar_wait(&bars[L::kRunEmpty + x], ((i >> 1) & 1) ^ 1, abort_flag, status, kStatusTmaWait)) break;
+                slot[x] = r;
+                mbar_arrive(&bars[L::kRunFull + x]);
             }
         }
     } else {
@@ -258,39 +297,57 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         float2 *xm = reinterpret_cast<float2 *>(smem + L::kXm);
         int sc = 0, oc[2] = {0, 0};
         bool ok = true;
-        for (int pos = pos0, taken; ok && pos < end; pos += taken) {
-            const PagesRun r = pages_run(p, work, blockIdx.x, pos, end, &taken);
+        // this thread's row of a run: the run's tiles, the keys it sees from the run's first on, where its
+        // result goes (an element of out, or a partial row), and half of its queries (by set)
+        constexpr int kC = D / 16;                                   // 16-byte chunks of half a row
+        struct Row {
+            int n, seen;
+            bool there, valid, busy, direct;                         // busy: the warp has rows
+            int64_t to;
+            uint4 x[kC];
+        };
+        auto fetch = [&](Row &w) {
+            PagesRun r;
+            w.there = feed.next(&r, true, lane, abort_flag, status);
+            if (!w.there) return;
             const PageSection &s = p.section[r.sec];
-            const bool valid = row < r.n_rows;
-            const bool busy = ((warp & 3) << 5) < r.n_rows;        // the warp has rows
-            const int place = r.row_tile * work.tile_tokens + (valid ? row / p.group : 0);
-            const int head = r.head * p.group + row % p.group;
+            w.n = r.n;
+            w.valid = row < r.n_rows;
+            w.busy = ((warp & 3) << 5) < r.n_rows;
+            const int in_tile = w.valid ? row / p.group : 0;
+            const int place = r.row_tile * work.tile_tokens + in_tile;
+            const int head = r.head * p.group + (w.valid ? row - in_tile * p.group : 0);
             const int token = query_token(p, s, place);
-            if (r.n > 0) {
-                // the row's queries, half of its channels per set, to their 128-byte-swizzled places
-                // (every score of the run before has been read: its products with Q are done)
-                constexpr int kC = D / 16;                           // 16-byte chunks of half a row
-                uint4 x[kC];
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(token) * p.q_stride +
-                                                                   head * D) + t * kC;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(token) * p.q_stride + head * D) + t * kC;
 #pragma unroll
-                for (int c = 0; c < kC; ++c) x[c] = valid ? src[c] : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < kC; ++c) w.x[c] = w.valid ? src[c] : make_uint4(0, 0, 0, 0);
+            w.seen = r.keys;
+            if (!r.common) w.seen = min(r.len, ((r.len - s.n_tokens + place) / p.block + 1) * p.block) - r.base;
+            w.seen -= r.begin * 128;
+            w.direct = r.whole && !r.common && s.common < 0;
+            w.to = w.direct ? static_cast<int64_t>(token) * p.out_stride + head * D
+                            : partial_row(p, work, r, blockIdx.x, row, static_cast<int64_t>(token) * p.heads + head);
+        };
+        Row now;
+        fetch(now);
+        while (ok && now.there) {
+            const int n = now.n, seen = now.seen;
+            const bool valid = now.valid, busy = now.busy, direct = now.direct;
+            const int64_t to = now.to;
+            if (n > 0) {
+                // the queries to their 128-byte-swizzled places (every score of the run before has been
+                // read: its products with Q are done)
 #pragma unroll
                 for (int c = 0; c < kC; ++c) {
                     const int cc = t * kC + c;                       // chunk of the whole row
-                    *reinterpret_cast<uint4 *>(smem + L::kQ + (cc >> 3) * L::kSub + row * 128 + (((cc & 7) ^ (row & 7)) << 4)) = x[c];
+                    *reinterpret_cast<uint4 *>(smem + L::kQ + (cc >> 3) * L::kSub + row * 128 +
+                                               (((cc & 7) ^ (row & 7)) << 4)) = now.x[c];
                 }
                 fence_proxy_async_shared();
                 tc_fence_before();
                 mbar_arrive(&bars[L::kQReady]);
             }
-            // keys the row sees, from the range's first
-            int seen = r.keys;
-            if (!r.common) {
-                const int at = r.len - s.n_tokens + place;
-                seen = min(r.len, (at / p.block + 1) * p.block) - r.base;
-            }
-            const int n_mine = (r.n + 1 - t) >> 1;
+            const int n_mine = (n + 1 - t) >> 1;
             float m_run = -INFINITY, l_run = 0.0f;
             for (int it = 0; it < n_mine; ++it, ++sc) {
                 ok = warp_wait_all(&bars[L::kSFull + t], sc & 1, abort_flag, status, kStatusSoftmaxWait);
@@ -299,7 +356,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     tc_fence_after();
                     ScoreRow x;
                     load_scores(s_tmem, x);
-                    const int cols = seen - (r.begin + 2 * it + t) * 128;
+                    const int cols = seen - (2 * it + t) * 128;
                     if (__any_sync(0xffffffffu, cols < 128)) mask_scores(x, cols);
                     const float m_tile = max_score(x) * p.scale_log2;
                     bool rescale = false;
@@ -321,7 +378,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
             // ---- both sets merged: thread (t, row) takes columns [t D / 2, (t + 1) D / 2)
             // (a warp whose wait ran out comes to the barrier too: all 256 threads leave together)
-            const bool has0 = r.n > 0, has1 = r.n > 1;
+            if (ok) fetch(now);                          // the next run's row, on its way meanwhile
+            const bool has0 = n > 0, has1 = n > 1;
             if (ok && has0) ok = warp_wait_all(&bars[L::kOFull + 0], oc[0]++ & 1, abort_flag, status, kStatusSoftmaxWait);
             if (ok && has1) ok = warp_wait_all(&bars[L::kOFull + 1], oc[1]++ & 1, abort_flag, status, kStatusSoftmaxWait);
             xm[t * 128 + row] = make_float2(m_run, l_run);
@@ -333,14 +391,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const float w0 = a0.x == -INFINITY ? 0.0f : ex2_approx(a0.x - m);
             const float w1 = a1.x == -INFINITY ? 0.0f : ex2_approx(a1.x - m);
             const float l = w0 * a0.y + w1 * a1.y;
-            const bool direct = r.whole && !r.common && s.common < 0;
             const uint32_t o0 = tmem + lane_base + 256 + t * (D / 2);
-            const int64_t out_row = static_cast<int64_t>(token) * p.heads + head;
-            const int64_t part = partial_row(p, work, r, blockIdx.x, row, out_row);
             if (busy && has0) {
                 const float inv = direct ? 1.0f / l : 1.0f;
-                uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + t * (D / 2);
-                float4 *prow = reinterpret_cast<float4 *>(p.part_o + part * D + t * (D / 2));
+                uint16_t *orow = p.out + to + t * (D / 2);
+                float4 *prow = reinterpret_cast<float4 *>(p.part_o + to * D + t * (D / 2));
 #pragma unroll 1
                 for (int cb = 0; cb < D / 64; ++cb) {
                     uint32_t v[32], v1[32];
@@ -374,7 +429,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                 }
             }
-            if (valid && !direct && t == 0) p.part_ml[part] = make_float2(m, l);
+            if (valid && !direct && t == 0) p.part_ml[to] = make_float2(m, l);
             tc_fence_before();
             named_bar_sync(1, 256);                  // xm and both accumulators have been read
         }

@@ -91,8 +91,8 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     const int worker = blockIdx.x * (blockDim.x >> 5) + warp;
     int pos = 0, end = 0;
     if (worker < work.workers) {
-        pos = static_cast<int>(static_cast<int64_t>(worker) * work.tiles / work.workers);
-        end = static_cast<int>(static_cast<int64_t>(worker + 1) * work.tiles / work.workers);
+        pos = static_cast<int>(first_place(work, worker));
+        end = static_cast<int>(first_place(work, worker + 1));
     }
     if (*p.v.version != p.v.expect) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.v.status, kStatusStale);
@@ -107,8 +107,7 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     const uint32_t my_piece = (lane & (D / 8 - 1)) ^ (my_key & 2) ^ ((my_key & 1) << 2);
     const uint32_t copy_to = stage0 + my_key * (D * 2);
     const uint32_t k_place = c ^ ((g & 6) ^ ((g & 1) << 2)), v_place = g ^ (2 * c);
-    for (int taken; pos < end; pos += taken) {
-        const PagesRun r = pages_run(p, work, worker, pos, end, &taken);
+    for (PagesRun r; next_run(p, work, worker, &pos, end, &r);) {
         const PageSection &s = p.section[r.sec];
 
         // ---- copies: page ids of the run, 32 at a time, the next 32 in flight (not waiting for the
@@ -317,13 +316,14 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
 // lanes at once, then the rows, four in flight.
 template <int D, bool HALF, int kS, int kM>
 __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p) {
-    grid_dependency_wait();
-    grid_launch_dependents();
-    if (*p.v.version != p.v.expect) return;
+    // (what the launch's parameters say is worked out before the partial results are there)
     const int lane = threadIdx.x & 31;
-    const int64_t out_row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (out_row >= static_cast<int64_t>(p.n_queries) * p.heads) return;
-    const int token = static_cast<int>(out_row / p.heads), head = static_cast<int>(out_row - static_cast<int64_t>(token) * p.heads);
+    const uint32_t out_row = blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (out_row >= static_cast<uint32_t>(p.n_queries) * p.heads) {
+        grid_dependency_wait();
+        return;
+    }
+    const int token = out_row / p.heads, head = out_row - token * p.heads;
     int lo = p.n_common, hi = p.n_sections;              // the section of the stream's own keys
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -332,8 +332,8 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
         else
             hi = mid;
     }
-    // pieces of the row's unit in both sections: the first worker, their number, the row of a later one
-    int n[2] = {0, 0}, first[2] = {0, 0};
+    // pieces of the row's unit in both sections: their number, the row of a later one
+    int n[2] = {0, 0};
     int64_t cut[2] = {0, 0};
     const int own = lo, common = p.section[lo].common;
 #pragma unroll
@@ -343,17 +343,20 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
         const PageSection &s = p.section[k ? common : own];
         const int place = k ? p.section[own].common_token + token - p.section[own].token0 : token - s.token0;
         const int rt = place / w.tile_tokens;
-        const int64_t a = s.start + (static_cast<int64_t>(rt) * p.v.kv_heads + head / p.group) * s.tiles;
-        first[k] = worker_of(w, a);
-        n[k] = worker_of(w, a + s.tiles - 1) - first[k] + 1;
-        cut[k] = w.cut_row + static_cast<int64_t>(first[k]) * w.cut_rows + (place - rt * w.tile_tokens) * p.group + head % p.group;
+        const uint32_t a = s.start + (rt * p.v.kv_heads + head / p.group) * (s.tiles + w.setup) + w.setup;
+        const int first = worker_of(w, a);
+        n[k] = worker_of(w, a + s.tiles - 1) - first + 1;
+        cut[k] = w.cut_row + static_cast<int64_t>(first) * w.cut_rows + (place - rt * w.tile_tokens) * p.group + head % p.group;
     }
     const int total = n[0] + n[1];
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (total == 1) return;                              // written by the attention kernel
+    const uint32_t version = *p.v.version;
     auto part_row = [&](int i) -> int64_t {              // i-th part
         const bool k = i >= n[0];
         const int piece = k ? i - n[0] : i;
-        if (piece == 0) return (k ? p.rows_common : 0) + out_row;
+        if (piece == 0) return (k ? p.rows_common : 0) + static_cast<int64_t>(out_row);
         return k ? cut[1] + static_cast<int64_t>(piece) * p.common.cut_rows : cut[0] + static_cast<int64_t>(piece) * p.own.cut_rows;
     };
     float m = -INFINITY, l = 0.0f;
@@ -401,6 +404,7 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
                 for (int i = 0; i < D / 32; ++i) acc[i] += wj[j] * x[j][i];
         }
     }
+    if (version != p.v.expect) return;
     const float inv = 1.0f / l;
     uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * (D / 32);
     if constexpr (D == 128)

@@ -15,53 +15,67 @@ struct PagesRun {
     int base;                    // place in the stream of its first key
     int len;                     // tokens of the stream
     int piece;                   // which piece of the unit this is (0: its first)
-    bool whole, common;          // the unit's only piece; keys of common pages
+    int whole, common;           // the unit's only piece; keys of common pages
 };
 
-// Worker that takes tile `pos`: the last one whose run begins at or before it, runs beginning
-// at floor(worker * tiles / workers).
-__device__ __forceinline__ int worker_of(const PageWork &w, int64_t pos) {
-    return static_cast<int>(((pos + 1) * w.workers - 1) / w.tiles);
+// First place of a worker's run, and the worker of a place: the last one whose run begins at or
+// before it.
+__device__ __forceinline__ uint32_t first_place(const PageWork &w, uint32_t worker) {
+    return worker * w.places / w.workers;
+}
+__device__ __forceinline__ int worker_of(const PageWork &w, uint32_t place) {
+    return static_cast<int>(((place + 1) * w.workers - 1) / w.places);
 }
 
+// The next run of a worker from place *pos on, *pos moved behind it; false if there is none
+// before `end`.
 template <int kS, int kM>
-__device__ __forceinline__ PagesRun pages_run(const PagesAttnParams<kS, kM> &p, const PageWork &w, int worker, int pos,
-                                              int end, int *taken) {
-    int lo = w.begin, hi = w.end;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.section[mid].start <= pos)
-            lo = mid;
-        else
-            hi = mid;
+__device__ __forceinline__ bool next_run(const PagesAttnParams<kS, kM> &p, const PageWork &w, int worker, int *pos,
+                                         int end, PagesRun *out) {
+    while (*pos < end) {
+        int lo = w.begin, hi = w.end;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (p.section[mid].start <= *pos)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const PageSection &s = p.section[lo];
+        const int span = s.tiles + w.setup;
+        const int unit = (*pos - s.start) / span;
+        const int at = *pos - s.start - unit * span;
+        const int taken = min(span - at, end - *pos);
+        const int first = *pos - at;                     // the unit's first place
+        *pos += taken;
+        if (at + taken <= w.setup) continue;             // the next worker's
+        PagesRun r;
+        r.sec = lo;
+        r.row_tile = unit / p.v.kv_heads;
+        r.head = unit - r.row_tile * p.v.kv_heads;
+        r.common = s.keys >= 0;
+        r.base = s.page0 << p.v.page_log2;
+        r.len = p.v.lengths[s.stream];
+        const int tokens = min(w.tile_tokens, s.n_tokens - r.row_tile * w.tile_tokens);
+        r.n_rows = tokens * p.group;
+        r.keys = r.common ? s.keys : r.len - r.base;
+        // KV tiles that the tile's rows see: all of the common keys, or up to its last token's
+        int seen = r.keys;
+        if (!r.common) {
+            const int last = r.len - s.n_tokens + r.row_tile * w.tile_tokens + tokens - 1;
+            seen = min(r.len, (last / p.block + 1) * p.block) - r.base;
+        }
+        const int tiles = (seen + (1 << w.tile_log2) - 1) >> w.tile_log2;
+        // (the unit's last piece takes what a longer stream has grown since the work was cut)
+        const bool last_piece = at + taken == span;
+        r.begin = max(0, at - w.setup);
+        r.n = max(0, (last_piece ? tiles : min(tiles, at + taken - w.setup)) - r.begin);
+        r.piece = at <= w.setup ? 0 : worker - worker_of(w, first + w.setup);
+        r.whole = r.piece == 0 && last_piece;
+        *out = r;
+        return true;
     }
-    const PageSection &s = p.section[lo];
-    PagesRun r;
-    r.sec = lo;
-    const int unit = (pos - s.start) / s.tiles;
-    r.begin = pos - s.start - unit * s.tiles;
-    *taken = min(s.tiles - r.begin, end - pos);
-    r.row_tile = unit / p.v.kv_heads;
-    r.head = unit - r.row_tile * p.v.kv_heads;
-    r.common = s.keys >= 0;
-    r.base = s.page0 << p.v.page_log2;
-    r.len = p.v.lengths[s.stream];
-    const int tokens = min(w.tile_tokens, s.n_tokens - r.row_tile * w.tile_tokens);
-    r.n_rows = tokens * p.group;
-    r.keys = r.common ? s.keys : r.len - r.base;
-    // KV tiles that the tile's rows see: all of the common keys, or up to its last token's
-    int seen = r.keys;
-    if (!r.common) {
-        const int last = r.len - s.n_tokens + r.row_tile * w.tile_tokens + tokens - 1;
-        seen = min(r.len, (last / p.block + 1) * p.block) - r.base;
-    }
-    const int tiles = (seen + (1 << w.tile_log2) - 1) >> w.tile_log2;
-    // (the unit's last piece takes what a longer stream has grown since the work was cut)
-    const bool last_piece = r.begin + *taken == s.tiles;
-    r.n = max(0, (last_piece ? tiles : min(tiles, r.begin + *taken)) - r.begin);
-    r.piece = r.begin == 0 ? 0 : worker - worker_of(w, pos - r.begin);
-    r.whole = r.begin == 0 && last_piece;
-    return r;
+    return false;
 }
 
 // Packed token of the `place`-th query token of a section.

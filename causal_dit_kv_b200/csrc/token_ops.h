@@ -92,7 +92,7 @@ struct PageWriteParams {
 // all its streams, or a stream's remaining keys with its own queries.  Units (row tile,
 // key head) of `tiles` KV tiles each, numbered row tile first.
 struct PageSection {
-    int32_t start;                        // place of its first tile among all the launch's tiles
+    int32_t start;                        // its first place among the launch's
     int32_t tiles;
     int32_t stream;                       // whose table row names the pages
     int32_t page0;                        // first page of the keys
@@ -101,11 +101,14 @@ struct PageSection {
     int32_t common, common_token;         // own keys: section of the common pages (-1: none), the first query's place there
 };
 
-// One launch's work: sections [begin, end), their units laid end to end in tiles of
-// 1 << tile_log2 keys and cut evenly into `workers` runs; a unit's later pieces leave their
-// rows at partial row cut_row + worker * cut_rows.
+// One launch's work: sections [begin, end).  Each unit takes `setup` places, for what a run costs
+// before and after its tiles, then one place per tile of 1 << tile_log2 keys; the units' places,
+// end to end, are cut evenly into `workers` runs (places x workers < 2^32).  A run that ends
+// within a unit's setup places leaves the unit to the next worker.  A unit's later pieces leave
+// their rows at partial row cut_row + worker * cut_rows.
 struct PageWork {
-    int32_t begin, end, tiles, workers, tile_log2, tile_tokens, cut_row, cut_rows;
+    int32_t begin, end, workers, setup, tile_log2, tile_tokens, cut_row, cut_rows;
+    uint32_t places;
     int32_t rows;                         // most query rows of a unit
 };
 
