@@ -400,8 +400,8 @@ template <typename P>
 bool cuts_units(const P &p, const PageWork &w) {
     for (int worker = 1, i = w.begin; worker < w.workers; ++worker) {
         const int64_t pos = static_cast<int64_t>(worker) * w.places / w.workers;
-        while (i + 1 < w.end && p.section[i + 1].start <= pos) ++i;
-        if ((pos - p.section[i].start) % (p.section[i].tiles + w.setup) > w.setup) return true;
+        while (i + 1 < w.end && p.start[i + 1] <= pos) ++i;
+        if ((pos - p.start[i]) % (p.section[i].tiles + w.setup) > w.setup) return true;
     }
     return false;
 }
@@ -441,6 +441,7 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
     int32_t section_of[kPagesMaxStreams];                    // of each group in this call (-1: none)
     int32_t place_of[kPagesMaxStreams];                      // first query's place of a stream among its section's
     p->n_members = 0;
+    p->tokens_each = -1;
     int n = 0;
     int32_t member_at = 0, most_common = 0;
     for (int g = 0; g < n_groups; ++g) {
@@ -468,6 +469,7 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
         int32_t place = 0;
         for (int32_t b = 0; b < c.streams; ++b) {
             if (h->group_of[b] != g || counts[b] == 0) continue;
+            p->tokens_each = p->tokens_each < 0 || p->tokens_each == counts[b] ? counts[b] : 0;
             p->member_first[p->n_members] = member_at;
             p->member_token[p->n_members++] = token_of[b];
             place_of[b] = place;
@@ -508,7 +510,7 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
         for (int i = begin; i < end; ++i) {
             PageSection &x = p->section[i];
             const int64_t keys = x.keys >= 0 ? x.keys : h->tokens[x.stream] - static_cast<int64_t>(x.page0) * c.page_tokens;
-            x.start = static_cast<int32_t>(std::min<int64_t>(places, INT32_MAX));
+            p->start[i] = static_cast<int32_t>(std::min<int64_t>(places, INT32_MAX));
             x.tiles = static_cast<int32_t>((keys + (1 << w.tile_log2) - 1) >> w.tile_log2);
             places += static_cast<int64_t>((x.n_tokens + w.tile_tokens - 1) / w.tile_tokens) * c.kv_heads * (x.tiles + w.setup);
         }

@@ -108,6 +108,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // (the first run's place, worked out by warp 3 before the launch's inputs are there)
+    int pos = 0, end = 0;
+    RunSpot spot;
+    bool more = false;
+    if (warp == 3) {
+        pos = static_cast<int>(first_place(work, blockIdx.x));
+        end = static_cast<int>(first_place(work, blockIdx.x + 1));
+        more = next_spot(p, work, &pos, end, &spot);
+    }
     grid_dependency_wait();                     // queries, pages and tables may come from the kernels before
     grid_launch_dependents();
 
@@ -270,21 +279,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         } else if (warp == 3 && lane == 0) {
             // ------------------------------------------------ the CTA's runs
-            int pos = static_cast<int>(first_place(work, blockIdx.x));
-            int end = static_cast<int>(first_place(work, blockIdx.x + 1));
             if (*p.v.version != p.v.expect) {    // (none: the tables are not those of the call)
                 if (blockIdx.x == 0) atomicOr(status, kStatusStale);
-                end = pos;
+                more = false;
             }
             PagesRun *slot = reinterpret_cast<PagesRun *>(smem + L::kRuns);
             PagesRun r;
             r.n = 0;
             for (int i = 0; r.n >= 0; ++i) {
                 const int x = i & 1;
-                if (!next_run(p, work, blockIdx.x, &pos, end, &r)) r.n = -1;
+                if (more)
+                    r = run_at(p, work, blockIdx.x, spot);
+                else
+                    r.n = -1;
                 if (!mbar_wait(&bars[L::kRunEmpty + x], ((i >> 1) & 1) ^ 1, abort_flag, status, kStatusTmaWait)) break;
                 slot[x] = r;
                 mbar_arrive(&bars[L::kRunFull + x]);
+                if (more) more = next_spot(p, work, &pos, end, &spot);
             }
         }
     } else {

@@ -84,20 +84,19 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     extern __shared__ __align__(16) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
-    // The launch before is the same call's other half, which had waited for everything before it
-    // when it let this one start: only the end of this grid has to come after its end.
-    if (!beside) grid_dependency_wait();
-    grid_launch_dependents();
     const int worker = blockIdx.x * (blockDim.x >> 5) + warp;
     int pos = 0, end = 0;
     if (worker < work.workers) {
         pos = static_cast<int>(first_place(work, worker));
         end = static_cast<int>(first_place(work, worker + 1));
     }
-    if (*p.v.version != p.v.expect) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.v.status, kStatusStale);
-        pos = end = 0;
-    }
+    RunSpot spot;
+    bool more = next_spot(p, work, &pos, end, &spot);
+    // The launch before is the same call's other half, which had waited for everything before it
+    // when it let this one start: only the end of this grid has to come after its end.
+    if (!beside) grid_dependency_wait();
+    grid_launch_dependents();
+    const bool stale = *p.v.version != p.v.expect;       // (looked at before anything is written)
     const int page_log2 = p.v.page_log2;
     // Piece x (16 bytes) of key y's row lies at place x ^ swizzle(y), swizzle(y) = (y & 6) ^ ((y & 1) << 2):
     // lanes of one access with keys 2i, 2i + 1 and four pieces each, or with two pieces of keys 2c,
@@ -107,7 +106,8 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     const uint32_t my_piece = (lane & (D / 8 - 1)) ^ (my_key & 2) ^ ((my_key & 1) << 2);
     const uint32_t copy_to = stage0 + my_key * (D * 2);
     const uint32_t k_place = c ^ ((g & 6) ^ ((g & 1) << 2)), v_place = g ^ (2 * c);
-    for (PagesRun r; next_run(p, work, worker, &pos, end, &r);) {
+    for (; more; more = next_spot(p, work, &pos, end, &spot)) {
+        const PagesRun r = run_at(p, work, worker, spot);
         const PageSection &s = p.section[r.sec];
 
         // ---- copies: page ids of the run, 32 at a time, the next 32 in flight (not waiting for the
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[b][x] += __shfl_xor_sync(0xffffffffu, l[b][x], d);
                 const int row = 8 * b + 2 * c + x;
-                if (row >= r.n_rows) continue;
+                if (row >= r.n_rows || stale) continue;
                 const int place = row / p.group, head = r.head * p.group + row - place * p.group;
                 const int token = query_token(p, s, place);
                 if (r.whole && !r.common && s.common < 0) {
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
                 }
             }
     }
+    if (stale && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.v.status, kStatusStale);
     if (beside) grid_dependency_wait();
 }
 
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
         const PageSection &s = p.section[k ? common : own];
         const int place = k ? p.section[own].common_token + token - p.section[own].token0 : token - s.token0;
         const int rt = place / w.tile_tokens;
-        const uint32_t a = s.start + (rt * p.v.kv_heads + head / p.group) * (s.tiles + w.setup) + w.setup;
+        const uint32_t a = p.start[k ? common : own] + (rt * p.v.kv_heads + head / p.group) * (s.tiles + w.setup) + w.setup;
         const int first = worker_of(w, a);
         n[k] = worker_of(w, a + s.tiles - 1) - first + 1;
         cut[k] = w.cut_row + static_cast<int64_t>(first) * w.cut_rows + (place - rt * w.tile_tokens) * p.group + head % p.group;

@@ -91,8 +91,7 @@ struct PageWriteParams {
 // One part of the attention's work: the keys of a group's common pages with the queries of
 // all its streams, or a stream's remaining keys with its own queries.  Units (row tile,
 // key head) of `tiles` KV tiles each, numbered row tile first.
-struct PageSection {
-    int32_t start;                        // its first place among the launch's
+struct alignas(32) PageSection {
     int32_t tiles;
     int32_t stream;                       // whose table row names the pages
     int32_t page0;                        // first page of the keys
@@ -128,8 +127,11 @@ struct PagesAttnParams {
     PageWork common, own;                 // the launches that take the common pages' sections and the streams'
     // groups' token order: member i is packed tokens member_token[i] .., at places member_first[i] ..
     int32_t n_members;
+    int32_t tokens_each;                  // query tokens of every member, if they are all alike (0: they are not)
     int32_t member_first[kMembers];
     int32_t member_token[kMembers];
+    // a section's first place among its launch's, apart from the rest: a search reads few lines of it
+    int32_t start[kSections];
     PageSection section[kSections];       // the groups' common pages, then the streams by their packed tokens
 };
 
