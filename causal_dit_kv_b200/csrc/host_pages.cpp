@@ -129,7 +129,7 @@ struct Edits {
     std::vector<std::pair<uint32_t, int32_t>> entries;
 
     template <int kE, int kR>
-    sdv2_status part(const sdv2_pages *h, size_t *c, size_t *x, size_t *l, size_t *e, cudaStream_t s) const {
+    sdv2_status part(const sdv2_pages *h, size_t *c, size_t *x, size_t *l, size_t *e, bool beside, cudaStream_t s) const {
         std::unique_ptr<PageEdits<kE, kR>> p(new PageEdits<kE, kR>);
         const PagesView w = h->view();
         p->table = w.table;
@@ -155,17 +155,19 @@ struct Edits {
             p->entry_at[p->n_entries] = entries[*e].first;
             p->entry[p->n_entries] = entries[*e].second;
         }
-        cudaError_t err = launch_page_edits(*p, s);
+        cudaError_t err = launch_page_edits(*p, beside, s);
         if (err != cudaSuccess) return cuda_fail(err, "page table launch");
         count_launch();
         return SDV2_OK;
     }
-    sdv2_status launch(const sdv2_pages *h, cudaStream_t s) const {
+    // beside: the launch before it is the same call's page copies
+    sdv2_status launch(const sdv2_pages *h, bool beside, cudaStream_t s) const {
         size_t c = 0, x = 0, l = 0, e = 0;
         const bool small = copies.size() <= 32 && clears.size() <= 32 && lengths.size() <= 32 && entries.size() <= 64;
         do {
-            const sdv2_status st = small ? part<64, 32>(h, &c, &x, &l, &e, s) : part<2000, 256>(h, &c, &x, &l, &e, s);
+            const sdv2_status st = small ? part<64, 32>(h, &c, &x, &l, &e, beside, s) : part<2000, 256>(h, &c, &x, &l, &e, beside, s);
             if (st != SDV2_OK) return st;
+            beside = false;
         } while (c < copies.size() || x < clears.size() || l < lengths.size() || e < entries.size());
         return SDV2_OK;
     }
@@ -351,7 +353,7 @@ sdv2_status extend(sdv2_pages *h, const int32_t *counts, cudaStream_t s) {
         }
         ed.lengths.emplace_back(b, h->tokens[b]);
     }
-    return ed.launch(h, s);
+    return ed.launch(h, false, s);
 }
 
 sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
@@ -619,8 +621,8 @@ sdv2_status fork(sdv2_pages *h, int32_t src, const int32_t *dst, int32_t n, int3
         ed.lengths.emplace_back(b, h->tokens[b]);
     }
     changed(h);
-    st = ed.launch(h, s);
-    return st != SDV2_OK || copied == 0 ? st : mv.launch(h, s);
+    if (copied > 0 && (st = mv.launch(h, s)) != SDV2_OK) return st;
+    return ed.launch(h, copied > 0, s);
 }
 
 sdv2_status free_streams(sdv2_pages *h, const int32_t *streams, int32_t n, cudaStream_t s) {
@@ -652,7 +654,7 @@ sdv2_status free_streams(sdv2_pages *h, const int32_t *streams, int32_t n, cudaS
         h->n_pages[b] = h->tokens[b] = 0;
     }
     changed(h);
-    return ed.launch(h, s);
+    return ed.launch(h, false, s);
 }
 
 sdv2_status compact(sdv2_pages *h, int32_t *used, cudaStream_t s) {
@@ -694,7 +696,7 @@ sdv2_status compact(sdv2_pages *h, int32_t *used, cudaStream_t s) {
     h->first_free = h->used;
     changed(h);
     st = mv.launch(h, s);
-    return st != SDV2_OK ? st : ed.launch(h, s);
+    return st != SDV2_OK ? st : ed.launch(h, true, s);
 }
 
 template <typename F>

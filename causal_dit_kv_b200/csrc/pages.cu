@@ -16,8 +16,11 @@
 namespace sdv2 {
 
 template <int kEntries, int kRows>
-__global__ void __launch_bounds__(256) page_edits_kernel(const __grid_constant__ PageEdits<kEntries, kRows> e) {
-    grid_dependency_wait();
+__global__ void __launch_bounds__(256)
+    page_edits_kernel(const __grid_constant__ PageEdits<kEntries, kRows> e, const bool beside) {
+    // The launch before may be the same call's page copies, which had waited for everything before
+    // them when they let this one start: only the end of this grid has to come after theirs.
+    if (!beside) grid_dependency_wait();
     grid_launch_dependents();
     const int i0 = blockIdx.x * blockDim.x + threadIdx.x, n = gridDim.x * blockDim.x;
     for (int c = 0; c < e.n_copies; ++c) {
@@ -32,12 +35,13 @@ __global__ void __launch_bounds__(256) page_edits_kernel(const __grid_constant__
     for (int i = i0; i < e.n_entries; i += n) e.table[e.entry_at[i]] = e.entry[i];
     for (int i = i0; i < e.n_lengths; i += n) e.lengths[e.length[i][0]] = e.length[i][1];
     if (i0 == 0) *e.version = e.new_version;
+    if (beside) grid_dependency_wait();
 }
 
 template <int kEntries, int kRows>
-cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, cudaStream_t s) {
+cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, bool beside, cudaStream_t s) {
     const int blocks = e.n_copies > 16 ? 16 : 1;
-    return launch_dependent(page_edits_kernel<kEntries, kRows>, dim3(blocks), dim3(256), 0, s, e);
+    return launch_dependent(page_edits_kernel<kEntries, kRows>, dim3(blocks), dim3(256), 0, s, e, beside);
 }
 
 constexpr int kMoveChunk = 16384;         // bytes of a page that one block copies: 256 threads x 4 x 16
@@ -131,8 +135,8 @@ cudaError_t launch_page_write(const PageWriteParams &p, cudaStream_t s) {
     return launch_dependent(page_write_kernel, dim3(static_cast<unsigned>((p.first[p.n] + 3) / 4)), dim3(128), 0, s, p);
 }
 
-template cudaError_t launch_page_edits<64, 32>(const PageEdits<64, 32> &, cudaStream_t);
-template cudaError_t launch_page_edits<2000, 256>(const PageEdits<2000, 256> &, cudaStream_t);
+template cudaError_t launch_page_edits<64, 32>(const PageEdits<64, 32> &, bool, cudaStream_t);
+template cudaError_t launch_page_edits<2000, 256>(const PageEdits<2000, 256> &, bool, cudaStream_t);
 template cudaError_t launch_page_moves<64>(const PageMoves<64> &, cudaStream_t);
 template cudaError_t launch_page_moves<2000>(const PageMoves<2000> &, cudaStream_t);
 

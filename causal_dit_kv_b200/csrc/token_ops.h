@@ -139,7 +139,7 @@ constexpr int kSmallSections = 40, kSmallMembers = 40;
 constexpr int kLargeSections = kPagesMaxStreams + kPagesMaxStreams / 2, kLargeMembers = kPagesMaxStreams;
 
 template <int kEntries, int kRows>
-cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, cudaStream_t s);
+cudaError_t launch_page_edits(const PageEdits<kEntries, kRows> &e, bool beside, cudaStream_t s);
 template <int kMoves>
 cudaError_t launch_page_moves(const PageMoves<kMoves> &m, cudaStream_t s);
 cudaError_t launch_page_write(const PageWriteParams &p, cudaStream_t s);
