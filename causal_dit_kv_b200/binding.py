@@ -385,11 +385,11 @@ def sdv2_prompt_check() -> int:
 
 def make_pages_config(streams, layers, heads, kv_heads, head_dim, pages, page_tokens=64, stream_pages=None,
                       max_queries=None, block_tokens=1, dtype="bf16") -> sdv2_pages_config:
-    """stream_pages None: as many as the pool has; max_queries None: one for every stream."""
+    """stream_pages None: as many as the pool has (within the limit); max_queries None: one for every stream."""
     cfg = sdv2_pages_config()
     cfg.streams, cfg.layers, cfg.heads, cfg.kv_heads, cfg.head_dim = streams, layers, heads, kv_heads, head_dim
     cfg.page_tokens, cfg.pages = page_tokens, pages
-    cfg.stream_pages = pages if stream_pages is None else stream_pages
+    cfg.stream_pages = min(pages, (1 << 25) // max(page_tokens, 1)) if stream_pages is None else stream_pages
     cfg.max_queries = streams if max_queries is None else max_queries
     cfg.block_tokens = min(block_tokens, (1 << 31) - 1)
     cfg.dtype = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)

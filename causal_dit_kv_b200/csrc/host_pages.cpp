@@ -58,9 +58,9 @@ sdv2_status check_config(const sdv2_pages_config *c) {
         return fail(SDV2_E_SHAPE, "page_tokens must be 16, 32, 64 or 128");
     if (c->pages < 1 || static_cast<int64_t>(c->pages) * c->kv_heads >= (1ll << 31))
         return fail(SDV2_E_SHAPE, "pages must be >= 1, pages x kv_heads < 2^31");
-    if (c->stream_pages < 1 || static_cast<int64_t>(c->stream_pages) * c->page_tokens >= (1ll << 30) ||
+    if (c->stream_pages < 1 || static_cast<int64_t>(c->stream_pages) * c->page_tokens > (1ll << 25) ||
         static_cast<int64_t>(c->stream_pages) * c->streams >= (1ll << 31))
-        return fail(SDV2_E_SHAPE, "stream_pages must be >= 1, x page_tokens < 2^30, x streams < 2^31");
+        return fail(SDV2_E_SHAPE, "stream_pages must be >= 1, x page_tokens <= 2^25, x streams < 2^31");
     if (c->max_queries < 1 || static_cast<int64_t>(c->max_queries) * c->heads >= (1ll << 29))
         return fail(SDV2_E_SHAPE, "max_queries must be >= 1, x heads < 2^29");
     if (c->block_tokens < 1) return fail(SDV2_E_SHAPE, "block_tokens must be >= 1");

@@ -99,8 +99,11 @@ sdv2_status prompt_attention(const sdv2_prompt_config *cfg, const void *q, const
     }
     if (n_seqs > 0 && (offsets[0] < 0 || offsets[n_seqs] > c.tokens))
         return fail(SDV2_E_ARG, "offsets must lie in 0..tokens");
-    for (int32_t i = 0; i < n_seqs; ++i)
+    for (int32_t i = 0; i < n_seqs; ++i) {
         if (offsets[i + 1] < offsets[i]) return fail(SDV2_E_ARG, "offsets must not decrease");
+        // (a CTA's work on one query tile stays well below the bound of its waits)
+        if (offsets[i + 1] - offsets[i] > (1 << 25)) return fail(SDV2_E_SHAPE, "a sequence has more than 2^25 tokens");
+    }
     if (n_seqs == 0 || offsets[n_seqs] == offsets[0]) return SDV2_OK;
     // a block longer than every sequence is the same mask as one that long (keeps the
     // kernel's (i / block + 1) * block below 2^31)

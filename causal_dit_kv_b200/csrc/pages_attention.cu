@@ -339,9 +339,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             w.to = w.direct ? static_cast<int64_t>(token) * p.out_stride + head * D
                             : partial_row(p, work, r, blockIdx.x, row, static_cast<int64_t>(token) * p.heads + head);
         };
+        // All 256 threads go on to a run, and leave, together: at a barrier that carries whether each
+        // of them has one (a warp whose wait ran out has none).
         Row now;
         fetch(now);
-        while (ok && now.there) {
+        bool go = named_bar_and(1, 256, now.there);
+        while (go) {
             const int n = now.n, seen = now.seen;
             const bool valid = now.valid, busy = now.busy, direct = now.direct;
             const int64_t to = now.to;
@@ -442,7 +445,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             if (valid && !direct && t == 0) p.part_ml[to] = make_float2(m, l);
             tc_fence_before();
-            named_bar_sync(1, 256);                  // xm and both accumulators have been read
+            go = named_bar_and(1, 256, now.there);       // (xm and both accumulators have been read)
         }
     }
 

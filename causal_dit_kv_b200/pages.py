@@ -43,6 +43,8 @@ class PagedKVCache:
         self.max_queries, self.block_tokens = self.cfg.max_queries, block_tokens
         self.dtype = _TORCH[dtype]
         self._views = {}
+        self._any = self.buffer.data_ptr()               # in place of the address that an empty tensor has not
+        self._scale = 1.0 / math.sqrt(head_dim)
 
     def close(self):
         if self.handle:
@@ -89,17 +91,15 @@ class PagedKVCache:
         arr, n = self._counts(counts), sum(counts)
         kp, ks = self._rows(k, "k", self.kv_heads, n)
         vp, vs = self._rows(v, "v", self.kv_heads, n)
-        if n:
-            B.sdv2_pages_write(self.handle, layer, kp, vp, ks, vs, arr, stream)
+        B.sdv2_pages_write(self.handle, layer, kp or self._any, vp or self._any, ks, vs, arr, stream)
 
     def attention(self, layer, q, out, counts, softmax_scale=None, stream=None):
         """Queries [sum counts, heads, d] of the last counts[b] tokens of each stream over all its keys."""
         arr, n = self._counts(counts), sum(counts)
         qp, qs = self._rows(q, "q", self.heads, n)
         op, os_ = self._rows(out, "out", self.heads, n)
-        if n:
-            scale = 1.0 / math.sqrt(self.head_dim) if softmax_scale is None else softmax_scale
-            B.sdv2_pages_attention(self.handle, layer, qp, op, qs, os_, arr, scale, stream)
+        B.sdv2_pages_attention(self.handle, layer, qp or self._any, op or self._any, qs, os_, arr,
+                               self._scale if softmax_scale is None else softmax_scale, stream)
 
     # -- views of the buffer (for inspection and tests)
     def _region(self, offset, dtype, *shape):

@@ -407,8 +407,8 @@ typedef struct {
  * q: device [T][Hq][d]; k, v: device [T][Hkv][d]; out: device [T][Hq][d], overlapping none
  *   of them.
  * offsets: HOST int64 [n_seqs + 1], not decreasing, in 0..T: sequence s is rows
- *   offsets[s] .. offsets[s+1] - 1.  Empty sequences are allowed; rows of out outside every
- *   sequence stay as they were.
+ *   offsets[s] .. offsets[s+1] - 1, at most 2^25 of them.  Empty sequences are allowed; rows of
+ *   out outside every sequence stay as they were.
  * Scores, softmax and sums are fp32; the probabilities are rounded to 16 bits before the
  * second product.  What lies outside a sequence, NaN and infinities included, has no part
  * in it; a value that is not finite inside a sequence may reach any row of that sequence.
@@ -434,7 +434,7 @@ typedef struct {
     int32_t head_dim;       /* d: 64 or 128 */
     int32_t page_tokens;    /* n: tokens of a page: 16, 32, 64 or 128 */
     int32_t pages;          /* P: pages of the pool (a page holds its tokens in every layer) */
-    int32_t stream_pages;   /* pages that one stream can have, at most; x page_tokens < 2^30 */
+    int32_t stream_pages;   /* pages that one stream can have, at most; x page_tokens <= 2^25 */
     int32_t max_queries;    /* query tokens of one attention call, all streams together */
     int32_t block_tokens;   /* b >= 1: attention is causal by blocks of b tokens (1: token by token) */
     int32_t dtype;          /* SDV2_DT_BF16 or SDV2_DT_FP16 */

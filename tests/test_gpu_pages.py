@@ -225,6 +225,94 @@ def test_two_groups_and_a_fork_of_a_fork():
     m.check()
 
 
+@pytest.mark.parametrize("page,dim,dtype", [(16, 128, "fp16"), (128, 64, "bf16"), (64, 128, "bf16")])
+def test_many_rows_over_long_and_short_keys(page, dim, dtype):
+    """The tile kernel's work cut inside units, units of one tile beside units of many, several row
+    tiles, and streams with different numbers of queries in one group."""
+    m = Model(**cfg(streams=9, heads=9, kv_heads=3, head_dim=dim, dtype=dtype, page_tokens=page, pages=900,
+                    max_queries=400))
+    m.grow([3000, 0, 0, 0, 40, 0, 700, 0, 0])
+    m.fork(0, [1, 2, 5])
+    m.fork(6, [7])
+    counts = [70, 1, 33, 0, 40, 129, 7, 18, 0]
+    m.grow([70, 1, 200, 0, 7, 129, 300, 18, 0])
+    m.attend(0, counts)
+    m.attend(0, [17, 17, 17, 0, 17, 17, 17, 17, 0])
+    m.grow([1] * 9)
+    m.attend(0, [2, 5, 1, 1, 3, 1, 1, 4, 1])          # few rows of their own, many in common
+    m.attend(0, [1, 1, 0, 1, 0, 1, 1, 0, 1])          # few rows both
+
+
+@pytest.mark.parametrize("streams,tokens", [(1, 30000), (2, 9000)])
+def test_long_keys_of_one_head(streams, tokens):
+    """One or two units over all workers: hundreds of pieces to merge."""
+    m = Model(**cfg(streams=streams, heads=4, kv_heads=1, head_dim=64, page_tokens=16, pages=streams * 1900,
+                    max_queries=64))
+    m.grow([tokens - 37 * b for b in range(streams)])
+    m.attend(0, [1] * streams)
+    m.attend(0, [30] * streams)
+
+
+def test_edits_and_moves_of_several_launches():
+    """More table entries, page copies and copies of one page than one launch's list holds."""
+    m = Model(**cfg(streams=120, layers=2, heads=1, kv_heads=1, head_dim=64, page_tokens=16, pages=9000))
+    m.grow([16 * 2100 if b == 0 else 0 for b in range(120)])
+    m.check()
+    m.fork(0, [5, 7], deep=True)                      # 2100 sources, 4200 copies
+    m.check()
+    m.grow([3 if b in (0, 5) else 0 for b in range(120)])
+    m.fork(5, [b for b in range(120) if b not in (0, 5, 7)])   # 117 copies of one page
+    m.check()
+    m.free([0, 7, 11])
+    m.compact()
+    m.check()
+    m.attend(0, [1 if b in (5, 6, 119) else 0 for b in range(120)])
+
+
+def test_two_caches_on_two_streams():
+    """Two handles' calls at once, each on a stream of its own."""
+    ms = [Model(seed=s, **cfg(streams=4, heads=4, kv_heads=2, head_dim=128, pages=400, max_queries=80))
+          for s in (1, 2)]
+    for m in ms:
+        m.grow([900, 0, 400, 1])
+        m.fork(0, [1])
+        m.grow([20, 20, 20, 20])
+    qs = [m.normal(80, 4, 128) for m in ms]
+    outs = [torch.empty_like(q) for q in qs]
+    streams = [torch.cuda.Stream() for _ in ms]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for m, q, out, stream in zip(ms, qs, outs, streams):
+            m.c.attention(0, q, out, [20] * 4, stream=stream)
+    torch.cuda.synchronize()
+    for m, q, out in zip(ms, qs, outs):
+        assert torch.equal(m.attend(0, [20] * 4, q=q), out)
+
+
+def test_graph_of_the_tile_kernel_follows_the_streams():
+    """A captured attention of many rows with a common prefix, replayed after its streams have grown
+    across pages and KV tiles."""
+    m = Model(**cfg(streams=3, heads=4, kv_heads=2, head_dim=64, pages=300, max_queries=60, block_tokens=20))
+    m.grow([500, 0, 0])
+    m.fork(0, [1, 2])
+    m.grow([20, 40, 160])
+    counts = [20, 20, 20]
+    q = m.normal(60, 4, 64)
+    out = torch.zeros_like(q)
+    m.c.attention(0, q, out, counts)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.c.attention(0, q, out, counts)
+    for step in range(12):
+        m.grow([20, 20, 60])
+        q.copy_(m.normal(60, 4, 64))
+        graph.replay()
+        m.attend(0, counts, q=q, run=lambda layer, q, o, c, s: o.copy_(out))
+    m.fork(0, [])                                     # nothing forked: the captured call stays good
+    graph.replay()
+    assert m.c.check() == 0
+
+
 def test_fork_whose_queries_reach_into_the_prefix():
     """Streams with nothing, or little, of their own: the common keys end before the first query."""
     m = Model(**cfg(streams=3, heads=4, kv_heads=2, head_dim=64, pages=60, max_queries=300))

@@ -29,7 +29,7 @@ def _prompt(B, offsets=(0, 8), scale=0.1, q=16, k=16, v=16, out=16, **kw):
     (dict(scale=float("nan")), "ARG"), (dict(scale=float("inf")), "ARG"), (dict(q=8), "ALIGN"), (dict(out=24), "ALIGN"),
     (dict(q=None), "ARG"), (dict(out=None), "ARG"), (dict(q_stride=255), "SHAPE"), (dict(k_stride=120), "SHAPE"),
     (dict(q_stride=260), "ALIGN"), (dict(out_stride=1 << 40), "SHAPE"), (dict(offsets=(0, 9)), "ARG"),
-    (dict(offsets=(-1, 8)), "ARG"), (dict(offsets=(0, 5, 4, 8)), "ARG")])
+    (dict(offsets=(-1, 8)), "ARG"), (dict(offsets=(0, (1 << 25) + 1), tokens=1 << 26), "SHAPE"), (dict(offsets=(0, 5, 4, 8)), "ARG")])
 def test_prompt_refusals(B, kw, status):
     with pytest.raises(B.SDV2Error) as e:
         _prompt(B, **kw)
@@ -53,7 +53,8 @@ def _pages(B, **kw):
 @pytest.mark.parametrize("kw", [
     dict(streams=0), dict(streams=257), dict(layers=0), dict(heads=7), dict(heads=129, kv_heads=1), dict(kv_heads=0),
     dict(heads=2048, kv_heads=2048), dict(head_dim=32), dict(page_tokens=48), dict(pages=0),
-    dict(pages=1 << 30, kv_heads=2), dict(stream_pages=0), dict(stream_pages=1 << 24), dict(max_queries=0),
+    dict(pages=1 << 30, kv_heads=2), dict(stream_pages=0), dict(stream_pages=1 << 24), dict(stream_pages=(1 << 19) + 1),
+    dict(max_queries=0),
     dict(max_queries=1 << 28), dict(block_tokens=0), dict(dtype=3)])
 def test_pages_config_refusals(B, kw):
     with pytest.raises(B.SDV2Error):
