@@ -63,7 +63,16 @@ sdv2_status launch_items(const sdv2_prompt_config &c, void *out, int64_t out_str
     p->block = c.block_tokens;
     p->pair_heads = pair ? 1 : 0;
     p->head_units = pair ? c.heads / 2 : c.heads;
+    p->n_items = n_items;
     p->n_units = n_items * p->head_units;
+    // Head units in as many chunks as keep a chunk's keys and values within 48 MB of the L2, so that
+    // they come from memory once (8192 tokens, 40 heads x 128, 168 MB: 271 MB read instead of 930,
+    // 766 us under the power limit instead of 810; 64, 32 and 20 MB: 769, 770 and 770).
+    int64_t keys = 0;
+    for (int i = 0; i < n_seqs; ++i) keys += len[i];
+    const int64_t kv_bytes = keys * c.kv_heads * c.head_dim * 4, chunk_bytes = 48ll << 20;
+    const int64_t chunks = std::min<int64_t>(p->head_units, (kv_bytes + chunk_bytes - 1) / chunk_bytes);
+    p->chunk_units = static_cast<int32_t>((p->head_units + chunks - 1) / chunks);
     p->scale_log2 = scale * 1.4426950408889634f;
     std::copy(first, first + n_seqs, p->seq_first);
     std::copy(len, len + n_seqs, p->seq_len);

@@ -62,7 +62,10 @@ struct PromptUnit {
 template <int kItems>
 __device__ __forceinline__ PromptUnit prompt_unit(const PromptParams<kItems> &p, int u) {
     PromptUnit w;
-    const int i = u / p.head_units, j = u - i * p.head_units;
+    // chunks of head units one after another, so that what runs at a time shares keys that fit the L2
+    const int chunk = u / (p.n_items * p.chunk_units), in = u - chunk * p.n_items * p.chunk_units;
+    const int width = min(p.chunk_units, p.head_units - chunk * p.chunk_units);
+    const int i = in / width, j = chunk * p.chunk_units + in - i * width;
     const uint32_t it = p.item[i];
     const int seq = it >> 24, tile = it & 0xffffffu;
     w.first = p.seq_first[seq];

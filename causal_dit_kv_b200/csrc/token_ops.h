@@ -12,13 +12,14 @@ constexpr int kPromptMaxSeqs = 256;       // sequences of one launch (a call tak
 constexpr int kPromptSmallItems = 256;    // items of the small and of the large parameter block
 constexpr int kPromptLargeItems = 6000;
 
-// Work units u = item * head_units + j.  pair_heads: unit j is query heads 2j and 2j + 1
+// Work units (item, j), j < head_units.  pair_heads: unit j is query heads 2j and 2j + 1
 // (one key head) on the item's 128 rows; otherwise head j on the item's 256 rows.
 template <int kItems>
 struct PromptParams {
     uint16_t *out;
     int64_t out_stride;                   // elements between tokens
-    int32_t group, block, pair_heads, head_units, n_units;
+    int32_t group, block, pair_heads, head_units, n_items, n_units;
+    int32_t chunk_units;                  // head units whose items are done before the next ones'
     float scale_log2;                     // softmax_scale * log2(e)
     int32_t seq_first[kPromptMaxSeqs];    // first token and tokens of each sequence
     int32_t seq_len[kPromptMaxSeqs];
