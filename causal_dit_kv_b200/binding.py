@@ -120,6 +120,7 @@ _SIGNATURES = [
     ("sdv2_pages_compact", c_int32, [c_void_p, POINTER(c_int32), c_void_p]),
     ("sdv2_pages_query", c_int32,
      [c_void_p, c_int32, POINTER(c_int32), POINTER(c_int32), c_int32, POINTER(c_int32), POINTER(c_int32)]),
+    ("sdv2_pages_share", c_int32, [c_void_p, c_int32]),
     ("sdv2_pages_used", c_int32, [c_void_p]),
     ("sdv2_pages_layout_get", c_int32, [c_void_p, POINTER(sdv2_pages_layout)]),
     ("sdv2_pages_check", c_int32, [c_void_p]),
@@ -472,6 +473,13 @@ def sdv2_pages_query(pages: int, stream_index: int):
     ids = (c_int32 * max(n.value, 1))()
     _check(lib().sdv2_pages_query(pages, stream_index, None, ids, n.value, None, None), "sdv2_pages_query")
     return int(tokens.value), list(ids)[:n.value], int(shared.value)
+
+
+SHARE_MODES = {"never": 0, "auto": 1, "always": 2}
+
+
+def sdv2_pages_share(pages: int, mode) -> None:
+    _check(lib().sdv2_pages_share(pages, SHARE_MODES[mode] if isinstance(mode, str) else int(mode)), "sdv2_pages_share")
 
 
 def sdv2_pages_used(pages: int) -> int:

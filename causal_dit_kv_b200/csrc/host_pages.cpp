@@ -86,6 +86,7 @@ struct sdv2_pages {
     // streams with the same first page, and the leading pages that all of them share
     // (kept until the next fork, free or compact: new pages are never shared ones)
     bool groups_known = false;
+    int32_t share = 1;                    // SDV2_SHARE_AUTO
     std::vector<int32_t> group_of;        // [streams]: its group, -1 none
     std::vector<int32_t> group_pages;
 
@@ -397,6 +398,22 @@ sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, in
     return SDV2_OK;
 }
 
+// Whether a group reads its common pages once for all of its `members`, with `rows` query rows to a
+// key head.  Apart, the members' reads meet in the L2, at 17 TB/s with few rows; once for all costs
+// a launch of the tile kernel (over 16 rows) and a merge of every row.  Measured with 300 keys of
+// each stream's own (us, apart / once): 64 streams of 32/8 heads x 128: 1024 common keys 30 / 31,
+// 2048 47 / 33, 8192 138 / 45; 16 streams: 1024 15 / 17, 2048 18 / 17, 8192 41 / 25; 4 streams of
+// 12 heads x 64, 16 tokens each: 2048 16 / 16, 8192 24 / 26.  16 rows or fewer: 16 streams of 12
+// heads x 128: 256 11.7 / 11.1, 8192 58 / 20; 4 streams of 32/8: 8192 17.5 / 19.
+bool shared(const sdv2_pages *h, int64_t members, int64_t pages, int64_t rows) {
+    if (h->share != SDV2_SHARE_AUTO) return h->share == SDV2_SHARE_ALWAYS;
+    const int64_t mb = 1 << 20;
+    const int64_t bytes = pages * h->cfg.page_tokens * h->cfg.kv_heads * h->cfg.head_dim * 4;
+    if (bytes > 64 * mb) return true;                        // the L2 does not hold it from one member to the next
+    const int64_t saved = (members - 1) * bytes;
+    return rows <= kRowsPerWorker ? members > 4 && saved >= 24 * mb : saved >= (30 + 4 * members) * mb;
+}
+
 // Whether the launch leaves any unit in pieces: a worker border inside one.
 template <typename P>
 bool cuts_units(const P &p, const PageWork &w) {
@@ -457,7 +474,7 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
             group_tokens += counts[b];
             pages = std::min(pages, (h->tokens[b] - counts[b]) / c.page_tokens);
         }
-        if (members < 2 || pages < 1) continue;
+        if (members < 2 || pages < 1 || !shared(h, members, pages, group_tokens * p->group)) continue;
         section_of[g] = n;
         PageSection &x = p->section[n++];
         x.stream = first;
@@ -508,20 +525,25 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
         w.cut_rows = few ? rows : 128;
         w.rows = rows;
         w.setup = few ? kSetupRows : kSetupTiles;
-        int64_t places = 0;
+        int64_t places = 0, units = 0;
         for (int i = begin; i < end; ++i) {
             PageSection &x = p->section[i];
             const int64_t keys = x.keys >= 0 ? x.keys : h->tokens[x.stream] - static_cast<int64_t>(x.page0) * c.page_tokens;
             p->start[i] = static_cast<int32_t>(std::min<int64_t>(places, INT32_MAX));
             x.tiles = static_cast<int32_t>((keys + (1 << w.tile_log2) - 1) >> w.tile_log2);
-            places += static_cast<int64_t>((x.n_tokens + w.tile_tokens - 1) / w.tile_tokens) * c.kv_heads * (x.tiles + w.setup);
+            const int64_t n_units = static_cast<int64_t>((x.n_tokens + w.tile_tokens - 1) / w.tile_tokens) * c.kv_heads;
+            units += n_units;
+            places += n_units * (x.tiles + w.setup);
         }
         w.places = static_cast<uint32_t>(std::min<int64_t>(places, INT32_MAX));
         const int64_t ctas = std::min(h->sm_count, kPagesMaxCtas);
         const int64_t most = few ? std::min<int64_t>(ctas * kRowWarps, kCutRows / rows) : ctas;
-        const int64_t shortest = w.setup + (few ? 4 : 2);    // places of a run, at least
+        // A unit to a worker while there are workers; longer units are cut into runs of at least so many
+        // places (two streams of 64 to 512 keys, 12 heads: 10.5 us with 7, 9.7 with 5, 7.3 with 3 or 2 in the
+        // row kernel; 16 streams on 2048 common keys: 20.0, 16.7, 19.9 us with 7, 4, 2 in the tile kernel)
+        const int64_t shortest = few ? 3 : 4;
         w.workers = static_cast<int32_t>(std::max<int64_t>(
-            1, std::min<int64_t>({most, (places + shortest - 1) / shortest, 0xffffffffll / (static_cast<int64_t>(w.places) + 1)})));
+            1, std::min<int64_t>({most, std::max(units, (places + shortest - 1) / shortest), 0xffffffffll / (static_cast<int64_t>(w.places) + 1)})));
         return w;
     };
     const int32_t cut = 2 * c.max_queries * c.heads;
@@ -542,7 +564,18 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
         if (e == cudaSuccess) count_launch();
     }
     if (e == cudaSuccess && (p->n_common > 0 || cuts_units(*p, p->own))) {
-        e = launch_pages_merge<kS, kM>(*p, half, s);
+        // most pieces of a unit, common and own together
+        int64_t pieces = 0;
+        for (int i = 0; i < n; ++i) {
+            const PageWork &w = i < p->n_common ? p->common : p->own;
+            const auto of = [&](int j, const PageWork &x) {
+                return static_cast<int64_t>(p->section[j].tiles) * x.workers / x.places + 2;
+            };
+            const int32_t common = p->section[i].common;
+            pieces = std::max(pieces, of(i, w) + (common >= 0 ? of(common, p->common) : 0));
+        }
+        const int64_t room = static_cast<int64_t>(h->sm_count) * 64 / (sum * c.heads);   // warps per row that run at once
+        e = launch_pages_merge<kS, kM>(*p, pieces > 40 && room >= 8 ? 8 : (pieces > 10 && room >= 4 ? 4 : 1), half, s);
         if (e == cudaSuccess) count_launch();
     }
     return e == cudaSuccess ? SDV2_OK : cuda_fail(e, "pages_attention launch");
@@ -791,6 +824,14 @@ sdv2_status sdv2_pages_query(sdv2_pages *h, int32_t stream, int32_t *tokens, int
         if (page_ids) std::copy(h->row(stream), h->row(stream) + std::min(capacity, h->n_pages[stream]), page_ids);
         return SDV2_OK;
     });
+}
+
+sdv2_status sdv2_pages_share(sdv2_pages *pages, int32_t mode) {
+    if (!pages) return fail(SDV2_E_ARG, "pages is NULL");
+    if (mode != SDV2_SHARE_NEVER && mode != SDV2_SHARE_AUTO && mode != SDV2_SHARE_ALWAYS)
+        return fail(SDV2_E_ARG, "mode must be SDV2_SHARE_NEVER, SDV2_SHARE_AUTO or SDV2_SHARE_ALWAYS");
+    pages->share = mode;
+    return SDV2_OK;
 }
 
 int32_t sdv2_pages_used(const sdv2_pages *pages) { return pages ? pages->used : -1; }

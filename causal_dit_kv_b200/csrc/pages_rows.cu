@@ -311,19 +311,18 @@ __global__ void __launch_bounds__(kRowWarps / 2 * 32, 2)
     if (beside) grid_dependency_wait();
 }
 
-// Merge of the partial results: a warp per output row (token, head).  Its parts are the
-// pieces of its unit of the stream's own keys and of its unit of the group's common keys;
-// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  The pieces' (m, l) are read by the
-// lanes at once, then the rows, four in flight.
-template <int D, bool HALF, int kS, int kM>
+// Merge of the partial results.  A row's parts are the pieces of its unit of the stream's own keys
+// and of its unit of the group's common keys; out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
+// kW warps take a row (token, head), each every kW-th part: the pieces' (m, l) are read by the lanes
+// at once, then the parts' rows, four in flight; the warps' results meet in shared memory.  A
+// long sequence of few heads is cut into a hundred pieces, which one warp took 17 us to read.
+template <int D, bool HALF, int kW, int kS, int kM>
 __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant__ PagesAttnParams<kS, kM> p) {
     // (what the launch's parameters say is worked out before the partial results are there)
-    const int lane = threadIdx.x & 31;
-    const uint32_t out_row = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (out_row >= static_cast<uint32_t>(p.n_queries) * p.heads) {
-        grid_dependency_wait();
-        return;
-    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kW;
+    const uint32_t n_rows = static_cast<uint32_t>(p.n_queries) * p.heads;
+    // (warps past the last row work on it too, and do not write)
+    const uint32_t my_row = blockIdx.x * (8 / kW) + warp / kW, out_row = min(my_row, n_rows - 1);
     const int token = out_row / p.heads, head = out_row - token * p.heads;
     int lo = p.n_common, hi = p.n_sections;              // the section of the stream's own keys
     while (hi - lo > 1) {
@@ -352,7 +351,6 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
     const int total = n[0] + n[1];
     grid_dependency_wait();
     grid_launch_dependents();
-    if (total == 1) return;                              // written by the attention kernel
     const uint32_t version = *p.v.version;
     auto part_row = [&](int i) -> int64_t {              // i-th part
         const bool k = i >= n[0];
@@ -364,8 +362,10 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
     float acc[D / 32];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) acc[i] = 0.0f;
-    for (int i0 = 0; i0 < total; i0 += 32) {
-        const float2 ml = i0 + lane < total ? p.part_ml[part_row(i0 + lane)] : make_float2(-INFINITY, 0.0f);
+    const int mine = (total - sub + kW - 1) / kW;        // this warp's parts: sub, sub + kW, ..
+    // (a single part's row was written by the attention kernel)
+    for (int i0 = 0; i0 < (total == 1 ? 0 : mine); i0 += 32) {
+        const float2 ml = i0 + lane < mine ? p.part_ml[part_row(sub + (i0 + lane) * kW)] : make_float2(-INFINITY, 0.0f);
         float mb = ml.x;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, o));
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
         for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
         l += lw;
         m = mb;
-        const int nb = min(32, total - i0);
+        const int nb = min(32, mine - i0);
         for (int j0 = 0; j0 < nb; j0 += 4) {
             float x[4][D / 32];
             float wj[4];
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
                 wj[j] = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
                 if (j0 + j >= nb) wj[j] = 0.0f;
                 if (wj[j] != 0.0f) {                     // (a part without keys has no output row)
-                    const float *src = p.part_o + part_row(i0 + j0 + j) * D + lane * (D / 32);
+                    const float *src = p.part_o + part_row(sub + (i0 + j0 + j) * kW) * D + lane * (D / 32);
                     if constexpr (D == 128)
                         *reinterpret_cast<float4 *>(x[j]) = *reinterpret_cast<const float4 *>(src);
                     else
@@ -405,7 +405,31 @@ __global__ void __launch_bounds__(256) pages_merge_kernel(const __grid_constant_
                 for (int i = 0; i < D / 32; ++i) acc[i] += wj[j] * x[j][i];
         }
     }
-    if (version != p.v.expect) return;
+    if constexpr (kW > 1) {
+        __shared__ float2 other_ml[8];
+        __shared__ float other[8][D];
+        if (lane == 0) other_ml[warp] = make_float2(m, l);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) other[warp][lane * (D / 32) + i] = acc[i];
+        __syncthreads();
+        if (sub != 0) return;
+        float top = m;
+#pragma unroll
+        for (int k = 1; k < kW; ++k) top = fmaxf(top, other_ml[warp + k].x);
+        const float c = m == -INFINITY ? 0.0f : exp2f(m - top);
+        l *= c;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] *= c;
+#pragma unroll
+        for (int k = 1; k < kW; ++k) {
+            const float2 ml = other_ml[warp + k];
+            const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+            l += w * ml.y;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] += w * other[warp + k][lane * (D / 32) + i];
+        }
+    }
+    if (my_row >= n_rows || total == 1 || version != p.v.expect) return;
     const float inv = 1.0f / l;
     uint16_t *orow = p.out + static_cast<int64_t>(token) * p.out_stride + head * D + lane * (D / 32);
     if constexpr (D == 128)
@@ -451,22 +475,27 @@ cudaError_t launch_pages_rows(const PagesAttnParams<kS, kM> &p, const PageWork &
     return half ? launch_rows_d<128, true>(p, w, beside, sm_count, s) : launch_rows_d<128, false>(p, w, beside, sm_count, s);
 }
 
-template <int kS, int kM>
-cudaError_t launch_pages_merge(const PagesAttnParams<kS, kM> &p, bool half, cudaStream_t s) {
+template <int D, bool HALF, int kS, int kM>
+static cudaError_t launch_merge_d(const PagesAttnParams<kS, kM> &p, int warps_per_row, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(p.n_queries) * p.heads;
-    const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
+    const dim3 grid(static_cast<unsigned>((rows * warps_per_row + 7) / 8));
+    if (warps_per_row == 1) return launch_dependent(pages_merge_kernel<D, HALF, 1, kS, kM>, grid, dim3(256), 0, s, p);
+    if (warps_per_row == 4) return launch_dependent(pages_merge_kernel<D, HALF, 4, kS, kM>, grid, dim3(256), 0, s, p);
+    return launch_dependent(pages_merge_kernel<D, HALF, 8, kS, kM>, grid, dim3(256), 0, s, p);
+}
+
+template <int kS, int kM>
+cudaError_t launch_pages_merge(const PagesAttnParams<kS, kM> &p, int warps_per_row, bool half, cudaStream_t s) {
     if (p.v.head_dim == 64)
-        return half ? launch_dependent(pages_merge_kernel<64, true, kS, kM>, grid, dim3(256), 0, s, p)
-                    : launch_dependent(pages_merge_kernel<64, false, kS, kM>, grid, dim3(256), 0, s, p);
-    return half ? launch_dependent(pages_merge_kernel<128, true, kS, kM>, grid, dim3(256), 0, s, p)
-                : launch_dependent(pages_merge_kernel<128, false, kS, kM>, grid, dim3(256), 0, s, p);
+        return half ? launch_merge_d<64, true>(p, warps_per_row, s) : launch_merge_d<64, false>(p, warps_per_row, s);
+    return half ? launch_merge_d<128, true>(p, warps_per_row, s) : launch_merge_d<128, false>(p, warps_per_row, s);
 }
 
 using SmallParams = PagesAttnParams<kSmallSections, kSmallMembers>;
 using LargeParams = PagesAttnParams<kLargeSections, kLargeMembers>;
 template cudaError_t launch_pages_rows(const SmallParams &, const PageWork &, bool, bool, int, cudaStream_t);
 template cudaError_t launch_pages_rows(const LargeParams &, const PageWork &, bool, bool, int, cudaStream_t);
-template cudaError_t launch_pages_merge(const SmallParams &, bool, cudaStream_t);
-template cudaError_t launch_pages_merge(const LargeParams &, bool, cudaStream_t);
+template cudaError_t launch_pages_merge(const SmallParams &, int, bool, cudaStream_t);
+template cudaError_t launch_pages_merge(const LargeParams &, int, bool, cudaStream_t);
 
 }  // namespace sdv2

@@ -154,6 +154,7 @@ template <int kSections, int kMembers>
 cudaError_t launch_pages_rows(const PagesAttnParams<kSections, kMembers> &p, const PageWork &w, bool half, bool beside,
                               int sm_count, cudaStream_t s);
 template <int kSections, int kMembers>
-cudaError_t launch_pages_merge(const PagesAttnParams<kSections, kMembers> &p, bool half, cudaStream_t s);
+cudaError_t launch_pages_merge(const PagesAttnParams<kSections, kMembers> &p, int warps_per_row, bool half,
+                               cudaStream_t s);
 
 }  // namespace sdv2

@@ -85,6 +85,10 @@ class PagedKVCache:
         """Moves the used pages to the front of the pool; returns their number."""
         return B.sdv2_pages_compact(self.handle, stream)
 
+    def share(self, mode):
+        """When the attention reads pages that forks share once for all: "auto" (where it is faster), "always", "never"."""
+        B.sdv2_pages_share(self.handle, mode)
+
     # -- the path
     def write(self, layer, k, v, counts, stream=None):
         """Keys and values [sum counts, kv_heads, d] of the last counts[b] tokens of each stream."""

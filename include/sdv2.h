@@ -504,8 +504,8 @@ sdv2_status sdv2_pages_write(sdv2_pages *pages, int32_t layer, const void *k, co
  *   between tokens (multiples of 8; 0: contiguous).  counts: HOST int32 [streams], >= 0 (0:
  *   the stream takes no part), their sum at most max_queries.  out overlaps no input.
  * Streams that share their leading pages (sdv2_pages_fork) have those read and multiplied
- * once for all of them: one group per first page, over the pages that all its streams have in
- * common.  Roundings as in sdv2_prompt_attention; what a page holds behind its stream's
+ * once for all of them, where that is faster (sdv2_pages_share): one group per first page,
+ * over the pages that all its streams have in common.  Roundings as in sdv2_prompt_attention; what a page holds behind its stream's
  * last token has no part in the result.
  * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN; SDV2_E_STATE if a stream has fewer
  * tokens; SDV2_E_CUDA. */
@@ -536,6 +536,12 @@ sdv2_status sdv2_pages_compact(sdv2_pages *pages, int32_t *used, sdv2_stream str
  * it has in common with all streams of its group (0: it shares none). */
 sdv2_status sdv2_pages_query(sdv2_pages *pages, int32_t stream, int32_t *tokens, int32_t *page_ids, int32_t capacity,
                              int32_t *n_pages, int32_t *shared_pages);
+
+/* When the attention reads a group's common pages once for all its streams: SDV2_SHARE_AUTO (as
+ * created) where the sizes say that it is faster, else always or never.  The results differ
+ * within the roundings only.  Errors: SDV2_E_ARG. */
+enum { SDV2_SHARE_NEVER = 0, SDV2_SHARE_AUTO = 1, SDV2_SHARE_ALWAYS = 2 };
+sdv2_status sdv2_pages_share(sdv2_pages *pages, int32_t mode);
 
 /* Used pages of the pool. */
 int32_t sdv2_pages_used(const sdv2_pages *pages);

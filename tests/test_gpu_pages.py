@@ -17,10 +17,11 @@ DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
 class Model:
     """The streams' tokens as plain tensors, page lists by the documented rule, beside the cache."""
 
-    def __init__(self, seed=1, dirty=True, **kw):
+    def __init__(self, seed=1, dirty=True, share="always", **kw):
         from causal_dit_kv_b200 import PagedKVCache
         self.kw = kw
         self.c = PagedKVCache(**kw)
+        self.c.share(share)
         self.gen = torch.Generator(device="cuda").manual_seed(seed)
         self.dtype = DT[kw.get("dtype", "bf16")]
         if dirty:                                     # what pages hold before they are written
@@ -203,6 +204,25 @@ def test_shared_prefix(prefix, heads, dim, dtype, new):
     counts[4] = counts[11] = 0
     m.attend(0, counts)
     m.attend(0, [new if b in (7, 8) else 0 for b in range(14)])       # one of the group alone
+
+
+@pytest.mark.parametrize("mode", ["auto", "never", "always"])
+@pytest.mark.parametrize("prefix,new", [(64, 1), (5000, 1), (5000, 9)])
+def test_sharing_modes(mode, prefix, new):
+    """Read once or apart, few rows and many: right either way; with more than 16 rows in common the
+    common keys are a launch of their own."""
+    from causal_dit_kv_b200 import binding as B
+    m = Model(share=mode, **cfg(streams=16, heads=8, kv_heads=8, head_dim=128, page_tokens=64, pages=200, max_queries=16 * new))
+    m.grow([prefix] + [0] * 15)
+    m.fork(0, list(range(1, 16)))
+    m.grow([new] * 16)
+    before = B.sdv2_launch_count()
+    m.attend(0, [new] * 16)
+    launches = B.sdv2_launch_count() - before
+    once = mode == "always" or (mode == "auto" and prefix == 5000)
+    # tiles for the common keys, rows for the streams' own, merge; otherwise rows and, if units are cut, merge
+    rows_in_common = 16 * new
+    assert launches == 3 if once and rows_in_common > 16 else launches <= 2
 
 
 def test_two_groups_and_a_fork_of_a_fork():

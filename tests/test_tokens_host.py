@@ -83,6 +83,7 @@ def test_pages_null_handles(B):
     assert lib.sdv2_pages_fork(None, 0, one, 1, 0, None) == B.SDV2_E_ARG
     assert lib.sdv2_pages_free(None, one, 1, None) == B.SDV2_E_ARG
     assert lib.sdv2_pages_compact(None, None, None) == B.SDV2_E_ARG
+    assert lib.sdv2_pages_share(None, 1) == B.SDV2_E_ARG
     assert lib.sdv2_pages_check(None) == B.SDV2_E_ARG and lib.sdv2_pages_used(None) == -1
     assert lib.sdv2_pages_destroy(None) == B.SDV2_OK
     with pytest.raises(B.SDV2Error) as e:
