@@ -19,6 +19,14 @@
 // started (clusterlaunchcontrol), so its set-up is paid once, the next unit's first tiles and
 // scores are under way while the last one's results are written, and SMs that run faster take more.
 // Every wait is bounded; a wait that runs out records itself in g_prompt_status.
+//
+// What bounds it: per 128 keys the two tiles' softmax (1930 cycles each, of which 1400 are the 128
+// exponentials a thread) and the round trip to the tensor core between them (score wait, four
+// products, 1500 cycles) overlap to 3400 cycles; tensor pipe 56 % and exponential unit 51 % busy.
+// Prompts of 77 to 4096 tokens, 32/8 heads of 128, bf16: 191 us in a burst (1.00 PFLOP/s), 221 us
+// (0.87) in a long run, which meets the 1000 W limit; 8192 tokens in blocks of 1024, 40 heads: 754 us
+// in a long run (1.03 PFLOP/s); 6289 tokens, 16/2 heads of 64, fp16: 53 us, where the products take
+// as long as with 128 channels for half the work; six prompts of 1 to 200 tokens, 12 heads: 10 us.
 #include <atomic>
 
 #include "attn_core.cuh"
@@ -28,35 +36,37 @@ namespace sdv2 {
 
 __device__ uint32_t g_prompt_status;
 
+struct PromptUnit {
+    int first, len;          // the sequence's tokens
+    int row0[2], head[2];    // each query tile's first row in the sequence, and its head
+    int n[2], n_max;         // KV tiles that each query tile sees (0: no such tile); n_max -1: no more units
+    int kv_head;
+};
+
 template <int D>
 struct PromptLayout {
     static constexpr int kTile = 128 * D * 2;             // bytes of a Q, K or V tile
     static constexpr int kSub = 128 * 128;                // its 64-column (128-byte) sub-tiles
     static constexpr int kKStages = D == 128 ? 2 : 4;
-    static constexpr int kVStages = D == 128 ? 3 : 4;
+    static constexpr int kVStages = D == 128 ? 2 : 4;     // (a third V tile of 128 channels gained nothing)
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + 2 * kTile;
     static constexpr int kV = kK + kKStages * kTile;
-    static constexpr int kBar = kV + kVStages * kTile;
+    static constexpr int kOut = kV + kVStages * kTile;    // 32 rows x 128 bytes of results for each softmax warp
+    static constexpr int kBar = kOut + 8 * 4096;
     static constexpr int kQFull = 0, kQEmpty = 1;
     static constexpr int kKFull = 2, kKEmpty = kKFull + kKStages;
     static constexpr int kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages;
     static constexpr int kSFull = kVEmpty + kVStages, kPFull = kSFull + 2, kOFull = kPFull + 2;
     static constexpr int kVAsk = kOFull + 2, kVFix = kVAsk + 1, kDrain = kVFix + 1;
-    // units: the current one is near its end, answer to a request landed, unit number published in a
-    // slot, slot read by every role
+    // units: the current one is near its end, answer to a request landed, unit published in a slot,
+    // slot read by every role
     static constexpr int kNear = kDrain + 1, kAnswer = kNear + 1, kUnitFull = kAnswer + 1, kUnitEmpty = kUnitFull + 2, kNumBars = kUnitEmpty + 2;
-    static constexpr int kUnits = kBar + ((kNumBars * 8 + 15) & ~15);   // the answer (16 bytes), two unit slots
-    static constexpr int kMisc = kUnits + 32;             // TMEM base, abort flag
+    static constexpr int kAnswerAt = kBar + ((kNumBars * 8 + 15) & ~15);   // 16 bytes
+    static constexpr int kUnits = kAnswerAt + 16;         // two unit slots
+    static constexpr int kMisc = kUnits + 2 * static_cast<int>(sizeof(PromptUnit));   // TMEM base, abort flag
     static constexpr int kAlloc = kMisc + 16 + 1024;      // room to align the base to 1024 bytes
     static_assert(kAlloc <= 232448, "shared memory of one CTA");
-};
-
-struct PromptUnit {
-    int first, len;          // the sequence's tokens
-    int row0[2], head[2];    // each query tile's first row in the sequence, and its head
-    int n[2], n_max;         // KV tiles that each query tile sees (0: no such tile)
-    int kv_head;
 };
 
 template <int kItems>
@@ -116,23 +126,24 @@ __device__ __forceinline__ int answered_cta(const void *answer) {
     return got ? static_cast<int>(x) : -1;
 }
 
-// A role's view of the CTA's units, in order.  The first is the CTA's own; later ones are
-// published by warp 3 in two slots.  Every role's thread (or warp, converged) calls next().
+// A role's view of the CTA's units, in order, as warp 3 publishes them in two slots (worked out
+// once: the divisions and the reads of the launch's lists took each role 2500 cycles a unit).
+// Every role's thread (or warp, converged) calls next().
 struct UnitFeed {
     uint64_t *full, *empty;
-    volatile int *slot;
+    const PromptUnit *slot;
     int n = 0;
-    // The next unit, or -1 at the end or when a wait ran out.  whole_warp: all lanes call it.
-    __device__ __forceinline__ int next(bool whole_warp, int lane, volatile uint32_t *abort, uint32_t *status) {
-        if (n++ == 0) return blockIdx.x;
-        const int x = n & 1, round = ((n - 2) >> 1) & 1;
+    // The next unit; false at the end or when a wait ran out.  whole_warp: all lanes call it.
+    __device__ __forceinline__ bool next(PromptUnit *w, bool whole_warp, int lane, volatile uint32_t *abort, uint32_t *status) {
+        const int x = n & 1, round = (n >> 1) & 1;
+        ++n;
         bool ok = mbar_wait(&full[x], round, abort, status, kStatusTmaWait);
         if (whole_warp) ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return -1;
-        const int u = slot[x];
+        if (!ok) return false;
+        *w = slot[x];
         if (whole_warp) __syncwarp();
         if (!whole_warp || lane == 0) mbar_arrive(&empty[x]);
-        return u;
+        return w->n_max >= 0;
     }
 };
 constexpr int kUnitReaders = 11;          // producer, MMA issuer, warp 2, eight softmax warps
@@ -168,13 +179,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    PromptUnit unit;                            // (warp 3's, worked out before the inputs are there)
+    if (warp == 3) unit = prompt_unit(p, blockIdx.x);
     grid_dependency_wait();                     // the inputs may come from the kernel just before
     grid_launch_dependents();
 
     UnitFeed feed;
     feed.full = &bars[L::kUnitFull];
     feed.empty = &bars[L::kUnitEmpty];
-    feed.slot = reinterpret_cast<volatile int *>(smem + L::kUnits + 16);
+    feed.slot = reinterpret_cast<const PromptUnit *>(smem + L::kUnits);
 
     if (warp < 4) {
         regs_dec<120>();                         // (104: 197 us for five ragged prompts, 80, where the issuer spills: 207; 120: 193)
@@ -182,8 +195,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // ------------------------------------------------ TMA producer
             int kc = 0, vc = 0, uc = 0;         // K tiles, V tiles and units issued so far
             bool ok = true;
-            for (int u; ok && (u = feed.next(false, lane, abort_flag, status)) >= 0; ++uc) {
-                const PromptUnit w = prompt_unit(p, u);
+            for (PromptUnit w; ok && feed.next(&w, false, lane, abort_flag, status); ++uc) {
                 ok = mbar_wait(&bars[L::kQEmpty], (uc & 1) ^ 1, abort_flag, status, kStatusTmaWait);
                 if (!ok) break;
                 mbar_arrive_expect_tx(&bars[L::kQFull], ((w.n[0] > 0) + (w.n[1] > 0)) * L::kTile);
@@ -252,8 +264,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             };
             int kc = 0, vc = 0, uc = 0, fixes = 0, pc[2] = {0, 0};
             bool ok = true;
-            for (int u; ok && (u = feed.next(false, lane, abort_flag, status)) >= 0; ++uc) {
-                const PromptUnit w = prompt_unit(p, u);
+            for (PromptUnit w; ok && feed.next(&w, false, lane, abort_flag, status); ++uc) {
                 ok = mbar_wait(&bars[L::kQFull], uc & 1, abort_flag, status, kStatusMmaWait) &&
                      mbar_wait(&bars[L::kKFull + kc % L::kKStages], (kc / L::kKStages) & 1, abort_flag, status,
                                kStatusMmaWait);
@@ -317,8 +328,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             // ------------------------------------------------ ends of sequences in V
             // (asked by the MMA issuer: a parity wait on the ring itself could be passed by)
             int vc = 0, fixes = 0;
-            for (int u; (u = feed.next(true, lane, abort_flag, status)) >= 0;) {
-                const PromptUnit w = prompt_unit(p, u);
+            for (PromptUnit w; feed.next(&w, true, lane, abort_flag, status);) {
                 vc += w.n_max;
                 const int valid = tail_rows(w);
                 if (valid == 0) continue;
@@ -328,23 +338,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (lane == 0) mbar_arrive(&bars[L::kVFix]);
             }
         } else if (warp == 3 && lane == 0) {
-            // ------------------------------------------------ further units
-            // (one request at a time, when the current unit is near its end: asked for earlier, long units
-            // would pile up on the CTAs that began with long ones; none after the first that finds no
-            // CTA left)
-            volatile int *slot = feed.slot;
-            for (int i = 0, u = 0; u >= 0; ++i) {
+            // ------------------------------------------------ the CTA's units
+            // (its own, then one request at a time, when the current unit is near its end: asked for
+            // earlier, long units would pile up on the CTAs that began with long ones; none after the
+            // first that finds no CTA left)
+            PromptUnit *slot = reinterpret_cast<PromptUnit *>(smem + L::kUnits);
+            for (int i = 0;; ++i) {
                 const int x = i & 1;
-                if (!mbar_wait(&bars[L::kNear], i & 1, abort_flag, status, kStatusTmaWait)) break;
-                mbar_arrive_expect_tx(&bars[L::kAnswer], 16);
-                request_cta(smem + L::kUnits, &bars[L::kAnswer]);
-                u = mbar_wait(&bars[L::kAnswer], i & 1, abort_flag, status, kStatusTmaWait)
-                        ? answered_cta(smem + L::kUnits)
-                        : -1;
-                fence_proxy_async_shared();      // the answer has been read before the next one is written
                 if (!mbar_wait(&bars[L::kUnitEmpty + x], ((i >> 1) & 1) ^ 1, abort_flag, status, kStatusTmaWait)) break;
-                slot[x] = u;
+                slot[x] = unit;
                 mbar_arrive(&bars[L::kUnitFull + x]);
+                if (unit.n_max < 0 || !mbar_wait(&bars[L::kNear], i & 1, abort_flag, status, kStatusTmaWait)) break;
+                mbar_arrive_expect_tx(&bars[L::kAnswer], 16);
+                request_cta(smem + L::kAnswerAt, &bars[L::kAnswer]);
+                const int u = mbar_wait(&bars[L::kAnswer], i & 1, abort_flag, status, kStatusTmaWait)
+                                  ? answered_cta(smem + L::kAnswerAt)
+                                  : -1;
+                fence_proxy_async_shared();      // the answer has been read before the next one is written
+                if (u >= 0)
+                    unit = prompt_unit(p, u);
+                else
+                    unit.n_max = -1;
             }
         }
     } else {
@@ -356,8 +370,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         const uint32_t s_tmem = tmem + lane_base + t * 128, o_tmem = tmem + lane_base + 256 + t * 128;
         int sc = 0, oc = 0;                          // score tiles and accumulators seen so far
         bool ok = true;
-        for (int u; ok && (u = feed.next(true, lane, abort_flag, status)) >= 0;) {
-            const PromptUnit w = prompt_unit(p, u);
+        for (PromptUnit w; ok && feed.next(&w, true, lane, abort_flag, status);) {
             const int n = t ? w.n[1] : w.n[0];
             if (n == 0) continue;
             const int i = (t ? w.row0[1] : w.row0[0]) + row;   // the row's place in its sequence
@@ -396,13 +409,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const float inv = 1.0f / l_run;
-            uint16_t *orow = p.out + static_cast<int64_t>(w.first + i) * p.out_stride + (t ? w.head[1] : w.head[0]) * D;
+            // 64 columns at a time through shared memory, so that eight lanes write 128 bytes of a row (a
+            // thread writing its own row touched 32 lines with every store: 4000 cycles a unit)
+            uint8_t *out_tile = smem + L::kOut + (warp - 4) * 4096;
+            const int row_first = (t ? w.row0[1] : w.row0[0]) + ((warp & 3) << 5);   // of the warp's rows
+            uint16_t *out = p.out + (t ? w.head[1] : w.head[0]) * D + (lane & 7) * 8;
+#pragma unroll 1
+            for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
-            for (int cb = 0; cb < D / 32; ++cb) {
-                uint32_t r[32];
-                tmem_ld32(o_tmem + cb * 32, r);
-                tmem_wait_ld_bind(r);
-                if (i < w.len) {
+                for (int cb = 0; cb < 2; ++cb) {
+                    uint32_t r[32];
+                    tmem_ld32(o_tmem + h * 64 + cb * 32, r);
+                    tmem_wait_ld_bind(r);
 #pragma unroll
                     for (int v = 0; v < 4; ++v) {
                         uint4 x;
@@ -410,9 +428,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         x.y = pack_16x2<HALF>(__uint_as_float(r[8 * v + 2]) * inv, __uint_as_float(r[8 * v + 3]) * inv);
                         x.z = pack_16x2<HALF>(__uint_as_float(r[8 * v + 4]) * inv, __uint_as_float(r[8 * v + 5]) * inv);
                         x.w = pack_16x2<HALF>(__uint_as_float(r[8 * v + 6]) * inv, __uint_as_float(r[8 * v + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(orow + cb * 32 + v * 8) = x;
+                        *reinterpret_cast<uint4 *>(out_tile + lane * 128 + (((cb * 4 + v) ^ (lane & 7)) << 4)) = x;
                     }
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int rr = 4 * k + (lane >> 3);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(out_tile + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+                    if (row_first + rr < w.len)
+                        *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(w.first + row_first + rr) * p.out_stride + h * 64) = x;
+                }
+                __syncwarp();
             }
             tc_fence_before();                       // (the next unit's first PV follows this thread's next arrival)
         }
