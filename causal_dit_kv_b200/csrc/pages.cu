@@ -1,15 +1,19 @@
 // The paged cache's table edits, page copies and writes.
 //
 // Table edits: a few integers, carried in the launch's parameters, so that tables change
-// in stream order without a host copy.  Bound by the launch.
+// in stream order without a host copy.  Bound by the launch; beside a call's page copies they
+// cost nothing of their own (a fork into 16 streams of 65 pages: 37.8 us with both, 42 in a row).
 //
 // Page copies: every page is one contiguous block per layer and side (keys, values), all
 // heads together; a block of threads takes 16 KB of it, reads that once and writes it to
-// every destination, so a fork into n streams reads its source once.  Bound by HBM.
+// every destination, so a fork into n streams reads its source once.  Bound by HBM: 16 copies of one
+// page of 30 layers (12 MB read, 189 written) 32 us; two calls that each move 32 such pages to the
+// front (1510 MB) 234.5 us with the calls around them, 99 % of the measured copy rate.
 //
 // Writes: one warp per new token; it looks up the token's stream, page and place once
-// and moves the token's keys and values, 16 bytes a lane.  Bound by HBM, for a step's few
-// tokens by the launch.
+// and moves the token's keys and values, 16 bytes a lane.  Bound by HBM: 8192 tokens of 40 heads
+// of 128 (336 MB moved) 56 us, 6.0 TB/s; for a step's few tokens by the launch: 64 tokens of 8
+// heads 8.7 us with the step's table edits.
 #include "ptx.cuh"
 #include "token_ops.h"
 

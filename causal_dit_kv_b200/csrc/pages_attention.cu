@@ -9,8 +9,8 @@
 // Few rows and many keys: the bound is HBM, so the work is cut evenly by keys.  All units
 // (128-row tile, key head) are laid end to end in KV tiles of 128 keys and every CTA, one per
 // SM, takes an equal run of tiles, crossing units as it goes; a unit cut by a border leaves
-// one partial result per CTA.  Rings of K and V tiles (192 KB at d = 128) keep loads in flight
-// across units.
+// one partial result per CTA.  Rings of three K and three V tiles (192 KB) of 128 channels, six and
+// six of 64, keep loads in flight across units.
 //   warp 0      looks up pages, one TMA box per page and 64 channels (a lane each)
 //   warp 1      MMA issuer: tile i of a run goes to accumulator set i & 1
 //   warp 2      zeroes the rows of a run's last V tile behind its keys
@@ -20,6 +20,12 @@
 //               out) and merge the two sets at the end
 // A query tile holds the rows (token, head of the group); rows beyond them cost no
 // exponentials.
+//
+// What bounds it with full tiles: the chain of a tile (scores, softmax, product) on two sets, and
+// a run's start and end (about five tiles' time, counted when the work is cut).  16 streams of 64
+// queries on 4000 common keys and up to 900 of their own, 12 heads of 64, fp16: 53.8 us, 35 MB read,
+// tensor pipe 26 %; 64 streams of one query on 16384 common keys, 40/8 heads of 128: 63 us with
+// the row kernel's part and the merge.
 #include <atomic>
 
 #include "attn_core.cuh"

