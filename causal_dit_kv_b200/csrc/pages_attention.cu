@@ -42,7 +42,10 @@ struct PagesLayout {
     static constexpr int kK = kQ + kTile;
     static constexpr int kV = kK + kStages * kTile;
     static constexpr int kXm = kQ;                        // (max, sum) of both sets, once the queries are done with
-    static constexpr int kBar = kV + kStages * kTile;
+    // 32 rows x 64 bytes of results for each softmax warp (at 128 channels the rings leave no room of
+    // its own: the queries' second half)
+    static constexpr int kOut = D == 128 ? kQ + kSub : kV + kStages * kTile;
+    static constexpr int kBar = kV + kStages * kTile + (D == 128 ? 0 : 8 * 2048);
     static constexpr int kQReady = 0;
     static constexpr int kKFull = 1, kKEmpty = kKFull + kStages;
     static constexpr int kVFull = kKEmpty + kStages, kVEmpty = kVFull + kStages;
@@ -414,8 +417,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             const uint32_t o0 = tmem + lane_base + 256 + t * (D / 2);
             if (busy && has0) {
                 const float inv = direct ? 1.0f / l : 1.0f;
-                uint16_t *orow = p.out + to + t * (D / 2);
-                float4 *prow = reinterpret_cast<float4 *>(p.part_o + to * D + t * (D / 2));
+                // 64 bytes a row at a time through shared memory, so that four lanes write them (a thread
+                // writing its own row touched 32 lines with every store)
+                uint8_t *out_tile = smem + L::kOut + (warp - 4) * 2048;
+                uint64_t mine = 0;                           // where the thread's row goes, 0: nowhere
+                if (valid)
+                    mine = direct ? reinterpret_cast<uint64_t>(p.out + to + t * (D / 2))
+                                  : reinterpret_cast<uint64_t>(p.part_o + to * D + t * (D / 2));
+                uint64_t dst[4];                             // of rows 8 k + lane / 4
+#pragma unroll
+                for (int k = 0; k < 4; ++k) dst[k] = __shfl_sync(0xffffffffu, mine, 8 * k + (lane >> 2));
+                auto put = [&](const uint32_t (&y)[16], int at) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(out_tile + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(y[4 * c], y[4 * c + 1], y[4 * c + 2], y[4 * c + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int rr = 8 * k + (lane >> 2), c = lane & 3;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(out_tile + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+                        if (dst[k] != 0) *reinterpret_cast<uint4 *>(dst[k] + at + c * 16) = x;
+                    }
+                    __syncwarp();
+                };
 #pragma unroll 1
                 for (int cb = 0; cb < D / 64; ++cb) {
                     uint32_t v[32], v1[32];
@@ -431,21 +456,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(w0 * __uint_as_float(v[i]) * inv);
                     }
-                    if (valid && direct) {
+                    uint32_t y[16];
+                    if (direct) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint4 y;
-                            y.x = pack_16x2<HALF>(__uint_as_float(v[8 * q]), __uint_as_float(v[8 * q + 1]));
-                            y.y = pack_16x2<HALF>(__uint_as_float(v[8 * q + 2]), __uint_as_float(v[8 * q + 3]));
-                            y.z = pack_16x2<HALF>(__uint_as_float(v[8 * q + 4]), __uint_as_float(v[8 * q + 5]));
-                            y.w = pack_16x2<HALF>(__uint_as_float(v[8 * q + 6]), __uint_as_float(v[8 * q + 7]));
-                            *reinterpret_cast<uint4 *>(orow + cb * 32 + q * 8) = y;
+                        for (int i = 0; i < 16; ++i)
+                            y[i] = pack_16x2<HALF>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        put(y, cb * 64);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = v[16 * h + i];
+                            put(y, cb * 128 + h * 64);
                         }
-                    } else if (valid) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            prow[cb * 8 + q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                                           __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
                     }
                 }
             }
