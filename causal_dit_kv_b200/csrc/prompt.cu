@@ -22,7 +22,7 @@
 //
 // What bounds it: per 128 keys the two tiles' softmax (1930 cycles each, of which 1400 are the 128
 // exponentials a thread) and the round trip to the tensor core between them (score wait, four
-// products, 1500 cycles) overlap to 3400 cycles; tensor pipe 56 % and exponential unit 51 % busy.
+// products, 1500 cycles) overlap to 3400 cycles; tensor pipe 57 % and exponential unit 52 % busy.
 // Prompts of 77 to 4096 tokens, 32/8 heads of 128, bf16: 191 us in a burst (1.00 PFLOP/s), 221 us
 // (0.87) in a long run, which meets the 1000 W limit; 8192 tokens in blocks of 1024, 40 heads: 754 us
 // in a long run (1.03 PFLOP/s); 6289 tokens, 16/2 heads of 64, fp16: 53 us, where the products take
