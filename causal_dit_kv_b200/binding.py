@@ -399,7 +399,7 @@ def make_pages_config(streams, layers, heads, kv_heads, head_dim, pages, page_to
 
 def int32_array(values):
     """Host integers as int32 values in memory."""
-    return values if isinstance(values, array) else array("i", values)
+    return values if isinstance(values, array) and values.typecode == "i" else array("i", values)
 
 
 def _address(values):

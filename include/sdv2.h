@@ -507,7 +507,7 @@ sdv2_status sdv2_pages_write(sdv2_pages *pages, int32_t layer, const void *k, co
  * once for all of them, where that is faster (sdv2_pages_share): one group per first page,
  * over the pages that all its streams have in common.  Roundings as in
  * sdv2_prompt_attention; what a page holds behind its stream's last token has no part in
- * the result.
+ * the result; a value that is not finite in a stream's tokens may reach any of its queries.
  * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN; SDV2_E_STATE if a stream has fewer
  * tokens; SDV2_E_CUDA. */
 sdv2_status sdv2_pages_attention(sdv2_pages *pages, int32_t layer, const void *q, void *out, int64_t q_stride,

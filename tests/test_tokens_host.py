@@ -92,3 +92,17 @@ def test_pages_null_handles(B):
     with pytest.raises(B.SDV2Error) as e:
         B.sdv2_pages_create(_pages(B), 256 * 1000, 1000)               # too small
     assert e.value.status == B.SDV2_E_ALIGN
+
+
+@pytest.mark.parametrize("code", ["b", "h", "i", "q", "I"])
+def test_host_integers_of_any_width(B, code):
+    from array import array
+    got = B.int32_array(array(code, [3, 0, 5]))
+    assert got.typecode == "i" and got.itemsize == 4 and list(got) == [3, 0, 5]
+
+
+def test_host_integers_refused(B):
+    with pytest.raises(OverflowError):
+        B.int32_array([1 << 31])
+    with pytest.raises(TypeError):
+        B.int32_array([1.5])
