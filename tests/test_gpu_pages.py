@@ -309,6 +309,22 @@ def test_two_caches_on_two_streams():
         assert torch.equal(m.attend(0, [20] * 4, q=q), out)
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, "fp16"), (128, "bf16")])
+def test_every_row_and_no_other_is_written(dim, dtype):
+    """Rows of partly filled tiles, written whole and as pieces; what lies between strided rows stays."""
+    m = Model(seed=7, **cfg(streams=5, heads=6, kv_heads=2, head_dim=dim, pages=400, max_queries=400, dtype=dtype))
+    m.grow([1500, 0, 0, 300, 40])
+    m.fork(0, [1, 2])
+    m.grow([50, 43, 1, 11, 6])
+    counts = [50, 43, 1, 11, 6]
+    q = m.normal(sum(counts), 6, dim)
+    room = torch.full((sum(counts) + 3, 8, dim), 5.0, dtype=q.dtype, device="cuda")
+    out = room[:sum(counts), :6]
+    m.c.attention(0, q, out, counts)
+    assert bool((room[:, 6:] == 5).all()) and bool((room[sum(counts):] == 5).all())
+    assert torch.equal(out, m.attend(0, counts, q=q))
+
+
 def test_graph_of_the_tile_kernel_follows_the_streams():
     """A captured attention of many rows with a common prefix, replayed after its streams have grown
     across pages and KV tiles."""

@@ -156,6 +156,55 @@ def test_same_bits_again_on_another_stream_and_from_a_graph():
         assert torch.equal(first, graphed)
 
 
+def test_calls_and_replays_at_once():
+    """Calls that run beside one another, each with more units than the device has SMs, take over
+    none but their own; the same for replays of their graphs."""
+    from causal_dit_kv_b200 import prompt_attention, prompt_check
+    cases = [(_inputs(20, 2600, 16, 4, 128, torch.bfloat16), [0, 2500, 2501, 2600]),
+             (_inputs(21, 3000, 12, 12, 64, torch.float16), [0, 1000, 3000]),
+             (_inputs(22, 1800, 24, 8, 128, torch.float16), [0, 1800])]
+    alone = [_check(*x, offsets, 1) for x, offsets in cases]
+    outs = [[torch.zeros_like(a) for _ in range(6)] for a in alone]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for (x, offsets), out, stream in zip(cases, outs, streams):
+            prompt_attention(*x, out[i], offsets, stream=stream)
+    torch.cuda.synchronize()
+    for a, out in zip(alone, outs):
+        assert all(torch.equal(a, o) for o in out)
+    graphs = [torch.cuda.CUDAGraph() for _ in cases]
+    for (x, offsets), out, graph in zip(cases, outs, graphs):
+        with torch.cuda.graph(graph):
+            for o in out[:3]:
+                prompt_attention(*x, o, offsets)
+    for out in outs:
+        for o in out:
+            o.zero_()
+    torch.cuda.synchronize()
+    for graph, stream in zip(graphs, streams):
+        with torch.cuda.stream(stream):
+            graph.replay()
+    torch.cuda.synchronize()
+    for a, out in zip(alone, outs):
+        assert all(torch.equal(a, o) for o in out[:3])
+    assert prompt_check() == 0
+
+
+def test_rows_behind_the_last_sequence_stay():
+    """Ends inside a tile, inside a warp's 32 rows and after a single row, both ways of pairing tiles."""
+    from causal_dit_kv_b200 import prompt_attention
+    for heads, d, dtype in [((4, 2), 128, torch.bfloat16), ((3, 3), 64, torch.float16)]:
+        for n in (1, 31, 33, 129, 200, 255):
+            q, k, v = _inputs(23, 400, *heads, d, dtype)
+            out = torch.full(q.shape, 5.0, dtype=dtype, device="cuda")
+            prompt_attention(q, k, v, out, [3, 3 + n])
+            assert bool((out[:3] == 5).all()) and bool((out[3 + n:] == 5).all())
+            short = torch.empty((n, heads[0], d), dtype=dtype, device="cuda")
+            prompt_attention(q[3:3 + n], k[3:3 + n], v[3:3 + n], short, [0, n])
+            assert torch.equal(out[3:3 + n], short)
+
+
 def test_wrapper_refusals():
     from causal_dit_kv_b200 import prompt_attention
     q, k, v = _inputs(11, 8, 4, 2, 64, torch.bfloat16)
