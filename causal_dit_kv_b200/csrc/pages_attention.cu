@@ -23,7 +23,7 @@
 //
 // What bounds it with full tiles: the chain of a tile (scores, softmax, product) on two sets, and
 // a run's start and end (about five tiles' time, counted when the work is cut).  16 streams of 64
-// queries on 4000 common keys and up to 900 of their own, 12 heads of 64, fp16: 52.9 us, 35 MB read,
+// queries on 4000 common keys and up to 900 of their own, 12 heads of 64, fp16: 52.3 us, 35 MB read,
 // tensor pipe 27 %; 64 streams of one query on 16384 common keys, 40/8 heads of 128: 62 us with
 // the row kernel's part and the merge.
 #include <atomic>
@@ -117,14 +117,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // (the first run's place, worked out by warp 3 before the launch's inputs are there)
+    // (the first run's place, and the run itself if its keys are common ones, worked out by warp 3
+    // before the launch's inputs are there)
     int pos = 0, end = 0;
     RunSpot spot;
-    bool more = false;
+    bool more = false, early = false;
+    PagesRun run;
     if (warp == 3) {
         pos = static_cast<int>(first_place(work, blockIdx.x));
         end = static_cast<int>(first_place(work, blockIdx.x + 1));
         more = next_spot(p, work, &pos, end, &spot);
+        early = more && p.section[spot.sec].keys >= 0;
+        if (early) run = run_at(p, work, blockIdx.x, spot);
     }
     grid_dependency_wait();                     // queries, pages and tables may come from the kernels before
     grid_launch_dependents();
@@ -288,23 +292,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         } else if (warp == 3 && lane == 0) {
             // ------------------------------------------------ the CTA's runs
-            if (*p.v.version != p.v.expect) {    // (none: the tables are not those of the call)
+            const uint32_t version = *p.v.version;
+            if (more && !early) run = run_at(p, work, blockIdx.x, spot);   // (both loads at once)
+            if (version != p.v.expect) {         // (none: the tables are not those of the call)
                 if (blockIdx.x == 0) atomicOr(status, kStatusStale);
                 more = false;
             }
             PagesRun *slot = reinterpret_cast<PagesRun *>(smem + L::kRuns);
-            PagesRun r;
-            r.n = 0;
-            for (int i = 0; r.n >= 0; ++i) {
+            for (int i = 0;; ++i) {
                 const int x = i & 1;
-                if (more)
-                    r = run_at(p, work, blockIdx.x, spot);
-                else
-                    r.n = -1;
+                if (!more) run.n = -1;
                 if (!mbar_wait(&bars[L::kRunEmpty + x], ((i >> 1) & 1) ^ 1, abort_flag, status, kStatusTmaWait)) break;
-                slot[x] = r;
+                slot[x] = run;
                 mbar_arrive(&bars[L::kRunFull + x]);
-                if (more) more = next_spot(p, work, &pos, end, &spot);
+                if (!more) break;
+                more = next_spot(p, work, &pos, end, &spot);
+                if (more) run = run_at(p, work, blockIdx.x, spot);
             }
         }
     } else {

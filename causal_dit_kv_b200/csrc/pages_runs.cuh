@@ -13,7 +13,7 @@ struct PagesRun {
     int begin, n;                // first KV tile of the run in the unit, tiles (0: nothing to read)
     int keys;                    // keys of the unit's page range (they end inside its last tile)
     int base;                    // place in the stream of its first key
-    int len;                     // tokens of the stream
+    int len;                     // tokens of the stream (common keys: 0, not needed)
     int piece;                   // which piece of the unit this is (0: its first)
     int whole, common;           // the unit's only piece; keys of common pages
 };
@@ -60,7 +60,8 @@ __device__ __forceinline__ bool next_spot(const PagesAttnParams<kS, kM> &p, cons
     return false;
 }
 
-// The run at a spot, with the stream's length as it is now.
+// The run at a spot, with the stream's length as it is now (common keys: from the launch's parameters
+// alone).
 template <int kS, int kM>
 __device__ __forceinline__ PagesRun run_at(const PagesAttnParams<kS, kM> &p, const PageWork &w, int worker, const RunSpot &o) {
     const PageSection &s = p.section[o.sec];
@@ -70,7 +71,7 @@ __device__ __forceinline__ PagesRun run_at(const PagesAttnParams<kS, kM> &p, con
     r.head = o.unit - r.row_tile * p.v.kv_heads;
     r.common = s.keys >= 0;
     r.base = s.page0 << p.v.page_log2;
-    r.len = p.v.lengths[s.stream];
+    r.len = r.common ? 0 : p.v.lengths[s.stream];
     const int tokens = min(w.tile_tokens, s.n_tokens - r.row_tile * w.tile_tokens);
     r.n_rows = tokens * p.group;
     r.keys = r.common ? s.keys : r.len - r.base;
