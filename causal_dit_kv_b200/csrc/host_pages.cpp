@@ -511,15 +511,15 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
     }
     p->n_sections = n;
 
-    // Both parts' kernels: a warp per run where no unit has more than 16 rows.  (The groups'
-    // units have at least as many rows as their streams'.)
+    // Both parts' kernels: a warp per run where no unit has more than 16 rows.  A stream outside every
+    // group may have more rows than the groups: one launch of the tile kernel takes both parts then.
     const int32_t own_rows = most_tokens * p->group, common_rows = most_common * p->group;
-    const bool few_own = own_rows <= kRowsPerWorker, few_common = common_rows <= kRowsPerWorker;
+    const bool few_own = own_rows <= kRowsPerWorker, few_common = few_own && common_rows <= kRowsPerWorker;
     auto work = [&](int begin, int end, bool few, int32_t rows, int32_t cut_row) {
         PageWork w{};
         w.begin = begin;
         w.end = end;
-        w.tile_log2 = few ? 4 : 7;
+        w.tile_log2 = few ? kRowKeysLog2 : kTileKeysLog2;
         w.tile_tokens = (few ? kRowsPerWorker : 128) / p->group;
         w.cut_row = cut_row;
         w.cut_rows = few ? rows : 128;

@@ -512,6 +512,7 @@ static cudaError_t launch_d(const PagesAttnParams<kS, kM> &p, const PageWork &w,
 template <int kS, int kM>
 cudaError_t launch_pages_tiles(const PagesAttnParams<kS, kM> &p, const PageWork &w, const CUtensorMap &tk,
                                const CUtensorMap &tv, bool half, cudaStream_t s) {
+    if (w.tile_log2 != kTileKeysLog2) return cudaErrorInvalidValue;
     if (p.v.head_dim == 64) return half ? launch_d<64, true>(p, w, tk, tv, s) : launch_d<64, false>(p, w, tk, tv, s);
     return half ? launch_d<128, true>(p, w, tk, tv, s) : launch_d<128, false>(p, w, tk, tv, s);
 }

@@ -474,6 +474,7 @@ static cudaError_t launch_rows_d(const PagesAttnParams<kS, kM> &p, const PageWor
 template <int kS, int kM>
 cudaError_t launch_pages_rows(const PagesAttnParams<kS, kM> &p, const PageWork &w, bool half, bool beside,
                               int sm_count, cudaStream_t s) {
+    if (w.tile_log2 != kRowKeysLog2 || w.rows > kRowsPerWorker) return cudaErrorInvalidValue;
     if (p.v.head_dim == 64)
         return half ? launch_rows_d<64, true>(p, w, beside, sm_count, s) : launch_rows_d<64, false>(p, w, beside, sm_count, s);
     return half ? launch_rows_d<128, true>(p, w, beside, sm_count, s) : launch_rows_d<128, false>(p, w, beside, sm_count, s);

@@ -1,8 +1,8 @@
 // How the paged attention's work is cut: the run of tiles that a worker (a CTA of the
 // tile kernel, a warp of the row kernel) takes within one unit, and where partial results go.
+// (Plain integer code: a test of the host's plans compiles it for the CPU.)
 #pragma once
 
-#include "ptx.cuh"
 #include "token_ops.h"
 
 namespace sdv2 {

@@ -37,6 +37,7 @@ constexpr int kPagesMaxStreams = 256;
 constexpr int kPagesMaxCtas = 160;        // attention CTAs of one launch, at most (scratch is sized for them)
 constexpr int kRowWarps = 8;              // warps of an SM in the few-row kernel, each a worker of its own
 constexpr int kRowsPerWorker = 16;        // query rows that one of them takes, at most
+constexpr int kRowKeysLog2 = 4, kTileKeysLog2 = 7;   // keys of a tile of the few-row and of the tile kernel
 
 // Status bits of the paged cache's word besides the waits of sdv2_internal.h.
 constexpr uint32_t kStatusStale = 1u << 5;   // a replayed call whose tables have been forked, freed or compacted since
@@ -145,7 +146,8 @@ template <int kMoves>
 cudaError_t launch_page_moves(const PageMoves<kMoves> &m, cudaStream_t s);
 cudaError_t launch_page_write(const PageWriteParams &p, cudaStream_t s);
 // The work w of a call by 128-row tiles on the tensor cores' own kernel (tiles of 128 keys),
-// or by at most kRowsPerWorker rows of one warp each (tiles of 16 keys).  `beside`: the launch
+// or by at most kRowsPerWorker rows of one warp each (tiles of 16 keys); work cut for the other
+// kernel is refused (cudaErrorInvalidValue).  `beside`: the launch
 // before it in the stream is the same call's other one, which it need not wait for to begin.
 template <int kSections, int kMembers>
 cudaError_t launch_pages_tiles(const PagesAttnParams<kSections, kMembers> &p, const PageWork &w, const CUtensorMap &tk,
