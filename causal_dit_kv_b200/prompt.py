@@ -16,7 +16,7 @@ _DTYPE = {torch.bfloat16: B.DT_BF16, torch.float16: B.DT_FP16}
 
 def rows_3d(x, name, heads, dim, dtype, device):
     """Check x [tokens, heads, dim] on CUDA device `device` (its index), a token's heads and channels
-    contiguous; returns (pointer, token stride, tokens)."""
+    contiguous, no two tokens overlapping; returns (pointer, token stride, tokens)."""
     shape, stride = x.shape, x.stride()
     if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {dim}], got {tuple(shape)}")
@@ -27,7 +27,9 @@ def rows_3d(x, name, heads, dim, dtype, device):
     tokens = shape[0]
     if stride[2] != 1 or (stride[1] != dim and heads > 1):
         raise ValueError(f"{name}: a token's heads and channels must be contiguous")
-    # (the stride of a single token is arbitrary)
+    # (the stride of a single token is arbitrary; 0, as of a broadcast tensor, would be "contiguous" to the library)
+    if tokens > 1 and stride[0] < heads * dim:
+        raise ValueError(f"{name}: tokens must not overlap or share their memory")
     return x.data_ptr(), (stride[0] if tokens > 1 else heads * dim), tokens
 
 
