@@ -83,6 +83,7 @@ struct sdv2_pages {
     int32_t used = 0;                     // pages with users
     int32_t first_free = 0;               // no page below it is free
     uint32_t version = 0;
+    bool torn = false;                    // some of a call's table edits were launched, others failed
     // streams with the same first page, and the leading pages that all of them share
     // (kept until the next fork, free or compact: new pages are never shared ones)
     bool groups_known = false;
@@ -92,11 +93,15 @@ struct sdv2_pages {
 
     int32_t *row(int32_t b) { return table.data() + static_cast<size_t>(b) * cfg.stream_pages; }
     int32_t pages_of(int64_t n) const { return static_cast<int32_t>((n + cfg.page_tokens - 1) / cfg.page_tokens); }
-    int32_t take() {                      // the lowest free page (there is one)
-        while (users[first_free] != 0) ++first_free;
-        users[first_free] = 1;
+    // The lowest free page from *at on (there is one), *at moved behind it: a call chooses its pages
+    // with an *at of its own, that of first_free, and takes them when its launches have succeeded.
+    int32_t next_free(int32_t *at) const {
+        while (users[*at] != 0) ++*at;
+        return (*at)++;
+    }
+    void take(int32_t p) {
+        users[p] = 1;
         ++used;
-        return first_free++;
     }
     void drop(int32_t p) {
         if (--users[p] == 0) {
@@ -122,6 +127,9 @@ struct sdv2_pages {
 
 namespace {
 
+// A call that changes the tables first works out its edits and copies, then launches them, and
+// only then changes the host's books: one that runs out of memory or whose launch fails changes nothing.
+
 // Table edits of one call, launched in as few kernels as they fit into.
 struct Edits {
     struct Copy { int32_t from, to, n; };
@@ -130,92 +138,98 @@ struct Edits {
     std::vector<std::pair<uint32_t, int32_t>> entries;
 
     template <int kE, int kR>
-    sdv2_status part(const sdv2_pages *h, size_t *c, size_t *x, size_t *l, size_t *e, bool beside, cudaStream_t s) const {
-        std::unique_ptr<PageEdits<kE, kR>> p(new PageEdits<kE, kR>);
+    sdv2_status parts(sdv2_pages *h, uint32_t version, bool beside, cudaStream_t s) const {
+        std::unique_ptr<PageEdits<kE, kR>> p(new PageEdits<kE, kR>);   // (one for all parts: a launch copies it)
         const PagesView w = h->view();
         p->table = w.table;
         p->lengths = w.lengths;
         p->version = w.version;
-        p->new_version = h->version;
+        p->new_version = version;
         p->width = w.width;
-        p->n_copies = p->n_clears = p->n_lengths = p->n_entries = 0;
-        for (; *c < copies.size() && p->n_copies < kR; ++*c, ++p->n_copies) {
-            p->copy[p->n_copies][0] = copies[*c].from;
-            p->copy[p->n_copies][1] = copies[*c].to;
-            p->copy[p->n_copies][2] = copies[*c].n;
-        }
-        for (; *x < clears.size() && p->n_clears < kR; ++*x, ++p->n_clears) {
-            p->clear[p->n_clears][0] = clears[*x].first;
-            p->clear[p->n_clears][1] = clears[*x].second;
-        }
-        for (; *l < lengths.size() && p->n_lengths < kR; ++*l, ++p->n_lengths) {
-            p->length[p->n_lengths][0] = lengths[*l].first;
-            p->length[p->n_lengths][1] = lengths[*l].second;
-        }
-        for (; *e < entries.size() && p->n_entries < kE; ++*e, ++p->n_entries) {
-            p->entry_at[p->n_entries] = entries[*e].first;
-            p->entry[p->n_entries] = entries[*e].second;
-        }
-        cudaError_t err = launch_page_edits(*p, beside, s);
-        if (err != cudaSuccess) return cuda_fail(err, "page table launch");
-        count_launch();
-        return SDV2_OK;
-    }
-    // beside: the launch before it is the same call's page copies
-    sdv2_status launch(const sdv2_pages *h, bool beside, cudaStream_t s) const {
         size_t c = 0, x = 0, l = 0, e = 0;
-        const bool small = copies.size() <= 32 && clears.size() <= 32 && lengths.size() <= 32 && entries.size() <= 64;
         do {
-            const sdv2_status st = small ? part<64, 32>(h, &c, &x, &l, &e, beside, s) : part<2000, 256>(h, &c, &x, &l, &e, beside, s);
-            if (st != SDV2_OK) return st;
-            beside = false;
+            const bool first = c + x + l + e == 0;
+            p->n_copies = p->n_clears = p->n_lengths = p->n_entries = 0;
+            for (; c < copies.size() && p->n_copies < kR; ++c, ++p->n_copies) {
+                p->copy[p->n_copies][0] = copies[c].from;
+                p->copy[p->n_copies][1] = copies[c].to;
+                p->copy[p->n_copies][2] = copies[c].n;
+            }
+            for (; x < clears.size() && p->n_clears < kR; ++x, ++p->n_clears) {
+                p->clear[p->n_clears][0] = clears[x].first;
+                p->clear[p->n_clears][1] = clears[x].second;
+            }
+            for (; l < lengths.size() && p->n_lengths < kR; ++l, ++p->n_lengths) {
+                p->length[p->n_lengths][0] = lengths[l].first;
+                p->length[p->n_lengths][1] = lengths[l].second;
+            }
+            for (; e < entries.size() && p->n_entries < kE; ++e, ++p->n_entries) {
+                p->entry_at[p->n_entries] = entries[e].first;
+                p->entry[p->n_entries] = entries[e].second;
+            }
+            const cudaError_t err = launch_page_edits(*p, beside && first, s);
+            if (err != cudaSuccess) {
+                h->torn = !first;
+                return cuda_fail(err, "page table launch");
+            }
+            count_launch();
         } while (c < copies.size() || x < clears.size() || l < lengths.size() || e < entries.size());
         return SDV2_OK;
     }
+    // version: the tables' new one; beside: the launch before it is the same call's page copies
+    sdv2_status launch(sdv2_pages *h, uint32_t version, bool beside, cudaStream_t s) const {
+        const bool small = copies.size() <= 32 && clears.size() <= 32 && lengths.size() <= 32 && entries.size() <= 64;
+        return small ? parts<64, 32>(h, version, beside, s) : parts<2000, 256>(h, version, beside, s);
+    }
 };
 
-// Page copies of one call: source src[i] to the pages dst[i].
+// Page copies of one call: source src[i] to the pages dst[i].  (Those are free ones until the
+// call's table edits are there.)
 struct Moves {
     std::vector<int32_t> src;
     std::vector<std::vector<int32_t>> dst;
 
     template <int kM>
-    sdv2_status part(const sdv2_pages *h, size_t *at, cudaStream_t s) const {
+    sdv2_status parts(const sdv2_pages *h, cudaStream_t s) const {
         std::unique_ptr<PageMoves<kM>> p(new PageMoves<kM>);
         p->base[0] = h->base + h->r.k;
         p->base[1] = h->base + h->r.v;
         p->layer_stride = static_cast<int64_t>(h->r.layer_stride);
         p->page_bytes = 2ll * h->cfg.kv_heads * h->cfg.page_tokens * h->cfg.head_dim;
         p->layers = h->cfg.layers;
-        p->n = 0;
         p->first[0] = 0;
-        for (; *at < src.size() && p->n < kM; ++*at, ++p->n) {
-            const std::vector<int32_t> &d = dst[*at];
-            int32_t f = p->first[p->n];
-            if (f + static_cast<int32_t>(d.size()) > kM) break;     // (d.size() <= 255: the first one always fits)
-            p->src[p->n] = src[*at];
-            for (int32_t x : d) p->dst[f++] = x;
-            p->first[p->n + 1] = f;
+        for (size_t at = 0; at < src.size();) {
+            p->n = 0;
+            for (; at < src.size() && p->n < kM; ++at, ++p->n) {
+                const std::vector<int32_t> &d = dst[at];
+                int32_t f = p->first[p->n];
+                if (f + static_cast<int32_t>(d.size()) > kM) break;     // (d.size() <= 255: the first one always fits)
+                p->src[p->n] = src[at];
+                for (int32_t x : d) p->dst[f++] = x;
+                p->first[p->n + 1] = f;
+            }
+            const cudaError_t err = launch_page_moves(*p, s);
+            if (err != cudaSuccess) return cuda_fail(err, "page copy launch");
+            count_launch();
         }
-        cudaError_t err = launch_page_moves(*p, s);
-        if (err != cudaSuccess) return cuda_fail(err, "page copy launch");
-        count_launch();
         return SDV2_OK;
     }
     sdv2_status launch(const sdv2_pages *h, cudaStream_t s) const {
         size_t total = 0;
         for (const auto &d : dst) total += d.size();
-        for (size_t at = 0; at < src.size();) {
-            const sdv2_status st = total <= 64 ? part<64>(h, &at, s) : part<2000>(h, &at, s);
-            if (st != SDV2_OK) return st;
-        }
-        return SDV2_OK;
+        return total <= 64 ? parts<64>(h, s) : parts<2000>(h, s);
     }
 };
 
+sdv2_status check_whole(const sdv2_pages *h) {
+    return h->torn ? fail(SDV2_E_STATE, "an earlier call's launches failed halfway: the device's page tables are lost")
+                   : SDV2_OK;
+}
+
 // The checks of a call that changes the tables.
 sdv2_status check_change(const sdv2_pages *h, cudaStream_t s) {
-    const sdv2_status st = check_device(h->device);
+    sdv2_status st = check_whole(h);
+    if (st == SDV2_OK) st = check_device(h->device);
     if (st != SDV2_OK) return st;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
     const cudaError_t e = cudaStreamIsCapturing(s, &cap);
@@ -345,16 +359,25 @@ sdv2_status extend(sdv2_pages *h, const int32_t *counts, cudaStream_t s) {
     Edits ed;
     ed.entries.reserve(static_cast<size_t>(need));
     ed.lengths.reserve(h->cfg.streams);
+    int32_t free = h->first_free;
     for (int32_t b = 0; b < h->cfg.streams; ++b) {
         if (counts[b] == 0) continue;
-        h->tokens[b] += counts[b];
-        for (const int32_t n = h->pages_of(h->tokens[b]); h->n_pages[b] < n; ++h->n_pages[b]) {
-            const int32_t p = h->row(b)[h->n_pages[b]] = h->take();
-            ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * h->cfg.stream_pages + h->n_pages[b]), p);
-        }
-        ed.lengths.emplace_back(b, h->tokens[b]);
+        const int32_t n = h->pages_of(static_cast<int64_t>(h->tokens[b]) + counts[b]);
+        for (int32_t i = h->n_pages[b]; i < n; ++i)
+            ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * h->cfg.stream_pages + i), h->next_free(&free));
+        ed.lengths.emplace_back(b, h->tokens[b] + counts[b]);
     }
-    return ed.launch(h, false, s);
+    if ((st = ed.launch(h, h->version, false, s)) != SDV2_OK) return st;
+    for (const auto &x : ed.entries) {
+        h->table[x.first] = x.second;
+        h->take(x.second);
+    }
+    h->first_free = free;
+    for (const auto &x : ed.lengths) {
+        h->tokens[x.first] = x.second;
+        h->n_pages[x.first] = h->pages_of(x.second);
+    }
+    return SDV2_OK;
 }
 
 sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, int64_t k_stride, int64_t v_stride,
@@ -384,7 +407,7 @@ sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, in
     }
     p.first[p.n] = at;
     if (sum == 0) return SDV2_OK;
-    if ((st = check_device(h->device)) != SDV2_OK) return st;
+    if ((st = check_whole(h)) != SDV2_OK || (st = check_device(h->device)) != SDV2_OK) return st;
     p.v = h->view();
     p.in[0] = static_cast<const uint16_t *>(k);
     p.in[1] = static_cast<const uint16_t *>(v);
@@ -601,7 +624,7 @@ sdv2_status attention(sdv2_pages *h, int32_t layer, const void *q, void *out, in
         active += counts[b] > 0;
     }
     if (sum == 0) return SDV2_OK;
-    if ((st = check_device(h->device)) != SDV2_OK) return st;
+    if ((st = check_whole(h)) != SDV2_OK || (st = check_device(h->device)) != SDV2_OK) return st;
     // (at most one group for every two active streams)
     return active + active / 2 <= kSmallSections && active <= kSmallMembers
                ? attend<kSmallSections, kSmallMembers>(h, layer, q, out, q_stride, out_stride, counts, sum, scale, s)
@@ -639,23 +662,33 @@ sdv2_status fork(sdv2_pages *h, int32_t src, const int32_t *dst, int32_t n, int3
         mv.src.push_back(h->row(src)[full + i]);
         mv.dst[i].reserve(n);
     }
+    int32_t free = h->first_free;
+    for (int32_t i = 0; i < n; ++i) {
+        const int32_t b = dst[i];
+        for (int32_t j = full; j < full + copied; ++j) {
+            const int32_t p = h->next_free(&free);
+            mv.dst[j - full].push_back(p);
+            ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * c.stream_pages + j), p);
+        }
+        if (full > 0) ed.copies.push_back({src, b, full});
+        ed.lengths.emplace_back(b, h->tokens[src]);
+    }
+    if (copied > 0 && (st = mv.launch(h, s)) != SDV2_OK) return st;
+    if ((st = ed.launch(h, h->version + 1, copied > 0, s)) != SDV2_OK) return st;
+    for (const auto &x : ed.entries) {
+        h->table[x.first] = x.second;
+        h->take(x.second);
+    }
+    h->first_free = free;
     for (int32_t i = 0; i < n; ++i) {
         const int32_t b = dst[i];
         std::copy(h->row(src), h->row(src) + full, h->row(b));
         for (int32_t j = 0; j < full; ++j) ++h->users[h->row(src)[j]];
-        for (int32_t j = 0; j < copied; ++j) {
-            const int32_t p = h->row(b)[full + j] = h->take();
-            mv.dst[j].push_back(p);
-            ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * c.stream_pages + full + j), p);
-        }
         h->n_pages[b] = h->n_pages[src];
         h->tokens[b] = h->tokens[src];
-        if (full > 0) ed.copies.push_back({src, b, full});
-        ed.lengths.emplace_back(b, h->tokens[b]);
     }
     changed(h);
-    if (copied > 0 && (st = mv.launch(h, s)) != SDV2_OK) return st;
-    return ed.launch(h, copied > 0, s);
+    return SDV2_OK;
 }
 
 sdv2_status free_streams(sdv2_pages *h, const int32_t *streams, int32_t n, cudaStream_t s) {
@@ -678,30 +711,34 @@ sdv2_status free_streams(sdv2_pages *h, const int32_t *streams, int32_t n, cudaS
     for (int32_t i = 0; i < n; ++i) {
         const int32_t b = streams[i];
         if (h->tokens[b] == 0) continue;
+        ed.clears.emplace_back(b, h->n_pages[b]);
+        ed.lengths.emplace_back(b, 0);
+    }
+    if ((st = ed.launch(h, h->version + 1, false, s)) != SDV2_OK) return st;
+    for (const auto &x : ed.clears) {
+        const int32_t b = x.first;
         for (int32_t j = 0; j < h->n_pages[b]; ++j) {
             h->drop(h->row(b)[j]);
             h->row(b)[j] = -1;
         }
-        ed.clears.emplace_back(b, h->n_pages[b]);
-        ed.lengths.emplace_back(b, 0);
         h->n_pages[b] = h->tokens[b] = 0;
     }
     changed(h);
-    return ed.launch(h, false, s);
+    return SDV2_OK;
 }
 
 sdv2_status compact(sdv2_pages *h, int32_t *used, cudaStream_t s) {
     if (!h) return fail(SDV2_E_ARG, "pages is NULL");
     const sdv2_pages_config &c = h->cfg;
-    if (used) *used = h->used;
+    if (used) *used = 0;
     bool any = false;
     for (int32_t p = h->used; p < c.pages && !any; ++p) any = h->users[p] > 0;
-    if (!any) return SDV2_OK;
-    sdv2_status st = check_change(h, s);
-    if (st != SDV2_OK) {
-        if (used) *used = 0;
-        return st;
+    if (!any) {
+        if (used) *used = h->used;
+        return check_whole(h);
     }
+    sdv2_status st = check_change(h, s);
+    if (st != SDV2_OK) return st;
     Edits ed;
     Moves mv;
     std::vector<int32_t> to(c.pages - h->used, -1);       // new place of page used + i
@@ -717,19 +754,20 @@ sdv2_status compact(sdv2_pages *h, int32_t *used, cudaStream_t s) {
     ed.entries.reserve(entries);
     for (int32_t b = 0; b < c.streams; ++b)
         for (int32_t j = 0; j < h->n_pages[b]; ++j) {
-            int32_t &p = h->row(b)[j];
-            if (p < h->used) continue;
-            p = to[p - h->used];
-            ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * c.stream_pages + j), p);
+            const int32_t p = h->row(b)[j];
+            if (p >= h->used)
+                ed.entries.emplace_back(static_cast<uint32_t>(static_cast<int64_t>(b) * c.stream_pages + j), to[p - h->used]);
         }
+    if ((st = mv.launch(h, s)) != SDV2_OK || (st = ed.launch(h, h->version + 1, true, s)) != SDV2_OK) return st;
+    for (const auto &x : ed.entries) h->table[x.first] = x.second;
     for (int32_t p : mv.src) {
         h->users[to[p - h->used]] = h->users[p];
         h->users[p] = 0;
     }
     h->first_free = h->used;
     changed(h);
-    st = mv.launch(h, s);
-    return st != SDV2_OK ? st : ed.launch(h, true, s);
+    if (used) *used = h->used;
+    return SDV2_OK;
 }
 
 template <typename F>

@@ -470,6 +470,10 @@ sdv2_status sdv2_pages_layout_of(const sdv2_pages_config *cfg, sdv2_pages_layout
  * on the host; the device's tables follow in stream order.  So the calls of one handle belong
  * on one stream, or on streams that the caller orders, and from one thread at a time; the
  * attention's scratch is shared by all its calls.
+ * A call that fails, for want of host memory (SDV2_E_STATE) or at a launch (SDV2_E_CUDA) among
+ * others, has changed no stream and no page that a stream has.  The one exception: if a call's table
+ * edits took several launches and a later one failed, the device's tables are lost, and every
+ * further call that reads or changes them is refused (SDV2_E_STATE).
  * CUDA graphs: sdv2_pages_write and sdv2_pages_attention can be captured.  A replay takes the
  * streams' lengths and pages of the time of the replay (as sdv2_pages_extend left them; the
  * captured split of the work stays right, though not as even, as streams grow).  A replay
@@ -486,7 +490,7 @@ sdv2_status sdv2_pages_destroy(sdv2_pages *pages);
  * lowest free pages in order (stream by stream).  The new tokens' keys and values are what
  * sdv2_pages_write puts there, layer by layer.
  * Errors: SDV2_E_ARG; SDV2_E_STATE without enough free pages, past stream_pages, or in
- * capture (nothing has changed then); SDV2_E_CUDA. */
+ * capture; SDV2_E_CUDA. */
 sdv2_status sdv2_pages_extend(sdv2_pages *pages, const int32_t *counts, sdv2_stream stream);
 
 /* Keys and values of the last counts[b] tokens of each stream b, in one layer.
@@ -518,8 +522,7 @@ sdv2_status sdv2_pages_attention(sdv2_pages *pages, int32_t layer, const void *q
  * pages, and its last page, if it is not full, is copied for each; deep 1: every page is
  * copied.  All layers; the copies take the lowest free pages in order.
  * Errors: SDV2_E_ARG (a stream out of range, src or a stream twice among dst);
- * SDV2_E_STATE (a dst that is not empty, too few free pages, capture; nothing has changed
- * then); SDV2_E_CUDA. */
+ * SDV2_E_STATE (a dst that is not empty, too few free pages, capture); SDV2_E_CUDA. */
 sdv2_status sdv2_pages_fork(sdv2_pages *pages, int32_t src, const int32_t *dst, int32_t n, int32_t deep,
                             sdv2_stream stream);
 

@@ -4,11 +4,13 @@
 //
 //   host_pages_main plan SEED N     plans of N random sessions cover every query's keys exactly once
 //   host_pages_main mixed           plans of calls that mix few and many query rows
+//   host_pages_main failures        calls that change the tables, with every allocation and launch failing in turn
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <new>
 #include <random>
 #include <string>
 
@@ -19,14 +21,37 @@ using std::min;
 #include "pages_runs.cuh"
 
 // ---------------------------------------------------------------- stand-ins
-static std::string g_error;
+static char g_error[512];
+
+// Allocations of a library call and launches that succeed until one fails (-1: none fails), and the launches made.
+static int g_good_allocations = -1, g_allocations = -1, g_good_launches = -1, g_made = 0;
+struct Armed {                                            // allocations count while one of these lives
+    Armed() { g_allocations = g_good_allocations; }
+    ~Armed() {
+        g_good_allocations = g_allocations;
+        g_allocations = -1;
+    }
+};
+__attribute__((noinline)) void *operator new(size_t n) {
+    if (g_allocations >= 0 && g_allocations-- == 0) throw std::bad_alloc();
+    void *p = std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+__attribute__((noinline)) void operator delete(void *p) noexcept { std::free(p); }
+__attribute__((noinline)) void operator delete(void *p, size_t) noexcept { std::free(p); }
+static cudaError_t launched() {
+    if (g_good_launches >= 0 && g_good_launches-- == 0) return cudaErrorLaunchOutOfResources;
+    ++g_made;
+    return cudaSuccess;
+}
 
 #define REQUIRE(x, ...)                                                        \
     do {                                                                       \
         if (!(x)) {                                                            \
-            std::printf("%s:%d: %s  ", __FILE__, __LINE__, #x);                \
-            std::printf("" __VA_ARGS__);                                       \
-            std::printf("  [last error: %s]\n", g_error.c_str());              \
+            std::printf("%s:%d: %s ", __FILE__, __LINE__, #x);                 \
+            std::printf(" " __VA_ARGS__);                                      \
+            std::printf("  [last error: %s]\n", g_error);              \
             std::exit(1);                                                      \
         }                                                                      \
     } while (0)
@@ -38,7 +63,7 @@ sdv2_status fail(sdv2_status st, const char *fmt, ...) {
     va_start(ap, fmt);
     std::vsnprintf(text, sizeof(text), fmt, ap);
     va_end(ap);
-    g_error = text;
+    std::snprintf(g_error, sizeof(g_error), "%s", text);
     return st;
 }
 sdv2_status cuda_fail(cudaError_t, const char *what) { return fail(SDV2_E_CUDA, "%s", what); }
@@ -90,6 +115,8 @@ static void keep(const LargeParams &p) { g_large = p, g_is_small = false; }
 namespace sdv2 {
 template <int kE, int kR>
 cudaError_t launch_page_edits(const PageEdits<kE, kR> &e, bool, cudaStream_t) {
+    const cudaError_t err = launched();
+    if (err != cudaSuccess) return err;
     for (int c = 0; c < e.n_copies; ++c)
         std::copy(e.table + static_cast<int64_t>(e.copy[c][0]) * e.width,
                   e.table + static_cast<int64_t>(e.copy[c][0]) * e.width + e.copy[c][2],
@@ -104,10 +131,19 @@ cudaError_t launch_page_edits(const PageEdits<kE, kR> &e, bool, cudaStream_t) {
     return cudaSuccess;
 }
 template <int kM>
-cudaError_t launch_page_moves(const PageMoves<kM> &, cudaStream_t) {
+cudaError_t launch_page_moves(const PageMoves<kM> &m, cudaStream_t) {
+    const cudaError_t err = launched();
+    if (err != cudaSuccess) return err;
+    for (int i = 0; i < m.n; ++i)
+        for (int j = m.first[i]; j < m.first[i + 1]; ++j)
+            for (int side = 0; side < 2; ++side)
+                for (int layer = 0; layer < m.layers; ++layer) {
+                    uint8_t *base = m.base[side] + layer * m.layer_stride;
+                    std::memcpy(base + m.dst[j] * m.page_bytes, base + m.src[i] * m.page_bytes, m.page_bytes);
+                }
     return cudaSuccess;
 }
-cudaError_t launch_page_write(const PageWriteParams &, cudaStream_t) { return cudaSuccess; }
+cudaError_t launch_page_write(const PageWriteParams &, cudaStream_t) { return launched(); }
 template <int kS, int kM>
 cudaError_t launch_pages_tiles(const PagesAttnParams<kS, kM> &p, const PageWork &w, const CUtensorMap &,
                                const CUtensorMap &, bool, cudaStream_t) {
@@ -146,12 +182,21 @@ struct Pool {
         std::free(memory);
     }
     Pool(const Pool &) = delete;
-    sdv2_status extend(const std::vector<int32_t> &counts) { return sdv2_pages_extend(h, counts.data(), nullptr); }
+    sdv2_status extend(const std::vector<int32_t> &counts) {
+        Armed armed;
+        return sdv2_pages_extend(h, counts.data(), nullptr);
+    }
     sdv2_status fork(int32_t src, const std::vector<int32_t> &dst, bool deep = false) {
+        Armed armed;
         return sdv2_pages_fork(h, src, dst.data(), static_cast<int32_t>(dst.size()), deep, nullptr);
     }
     sdv2_status free(const std::vector<int32_t> &s) {
+        Armed armed;
         return sdv2_pages_free(h, s.data(), static_cast<int32_t>(s.size()), nullptr);
+    }
+    sdv2_status compact() {
+        Armed armed;
+        return sdv2_pages_compact(h, nullptr, nullptr);
     }
     sdv2_status attend(const std::vector<int32_t> &counts) {
         g_launches.clear();
@@ -365,7 +410,7 @@ static void sessions(uint64_t seed, int n) {
             } else if (what < 8) {
                 REQUIRE(pool.free({pick(0, streams - 1)}) == SDV2_OK);
             } else if (what < 9) {
-                REQUIRE(sdv2_pages_compact(pool.h, nullptr, nullptr) == SDV2_OK);
+                REQUIRE(pool.compact() == SDV2_OK);
             }
             pool.check_books();
             // queries of every stream alike, or different numbers, or few streams
@@ -389,10 +434,140 @@ static void sessions(uint64_t seed, int n) {
     }
 }
 
+// ---------------------------------------------------------------- failures
+// What a user of the pool can tell of it: tables, lengths, and the contents of the pages that streams have.
+static std::string picture(const Pool &pool) {
+    std::string out;
+    const sdv2_pages_config &c = pool.c;
+    const int64_t page_bytes = 2ll * c.kv_heads * c.page_tokens * c.head_dim;
+    for (int32_t b = 0; b < c.streams; ++b) {
+        int32_t tokens = 0, n = 0, shared = 0;
+        REQUIRE(sdv2_pages_query(pool.h, b, &tokens, nullptr, 0, &n, &shared) == SDV2_OK);
+        std::vector<int32_t> ids(n + 1);
+        REQUIRE(sdv2_pages_query(pool.h, b, nullptr, ids.data(), n, nullptr, nullptr) == SDV2_OK);
+        out += std::to_string(tokens) + "/" + std::to_string(shared) + ":";
+        for (int32_t i = 0; i < n; ++i) {
+            out += std::to_string(ids[i]) + " ";
+            for (uint64_t side : {pool.h->r.k, pool.h->r.v})
+                out.append(reinterpret_cast<char *>(pool.h->base + side) + ids[i] * page_bytes, page_bytes);
+        }
+    }
+    return out + "|" + std::to_string(sdv2_pages_used(pool.h)) + "|" + std::to_string(pool.h->version);
+}
+
+static void fill_pages(const Pool &pool) {
+    const int64_t page_bytes = 2ll * pool.c.kv_heads * pool.c.page_tokens * pool.c.head_dim;
+    for (uint64_t side : {pool.h->r.k, pool.h->r.v})
+        for (int64_t i = 0; i < pool.c.pages * page_bytes; ++i)
+            pool.h->base[side + i] = static_cast<uint8_t>((i * 2654435761u >> 13) + i / page_bytes + (side ? 7 : 0));
+}
+
+// Does `call` on a fresh pool made by `start`, every allocation failing in turn, then every launch: a call
+// that fails leaves the pool as it was, unless its table edits had begun.  `launches`: of a call that succeeds.
+template <typename Start, typename Call>
+static void every_failure(const sdv2_pages_config &c, Start start, Call call, int launches) {
+    std::string before, after;
+    int allocations = 0;
+    {
+        Pool pool(c);
+        start(pool);
+        fill_pages(pool);
+        before = picture(pool);
+        g_made = 0;
+        g_good_allocations = 1 << 30;
+        REQUIRE(call(pool) == SDV2_OK);
+        allocations = (1 << 30) - g_good_allocations;
+        g_good_allocations = -1;
+        REQUIRE(g_made == launches && allocations > 0, "%d launches", g_made);
+        pool.check_books();
+        after = picture(pool);
+        REQUIRE(before != after);
+    }
+    const int every = max(1, allocations / 5);            // (of thousands of like ones a few, and the last ones)
+    for (int i = 0; i <= allocations; i += i + every < allocations - 4 ? every : 1) {
+        Pool pool(c);
+        start(pool);
+        fill_pages(pool);
+        g_good_allocations = i;
+        REQUIRE(call(pool) == (i == allocations ? SDV2_OK : SDV2_E_STATE));
+        g_good_allocations = -1;
+        pool.check_books();
+        REQUIRE(picture(pool) == (i == allocations ? after : before), "allocation %d", i);
+        if (i < allocations) {                            // and again, with memory
+            REQUIRE(call(pool) == SDV2_OK);
+            pool.check_books();
+            REQUIRE(picture(pool) == after);
+        }
+    }
+    for (int good = 0; good < launches; ++good) {
+        Pool pool(c);
+        start(pool);
+        fill_pages(pool);
+        g_good_launches = good;
+        const uint32_t version = *reinterpret_cast<uint32_t *>(pool.h->base + pool.h->r.version);
+        const std::vector<int32_t> lengths(reinterpret_cast<int32_t *>(pool.h->base + pool.h->r.length),
+                                           reinterpret_cast<int32_t *>(pool.h->base + pool.h->r.length) + c.streams);
+        REQUIRE(call(pool) == SDV2_E_CUDA);
+        g_good_launches = -1;
+        REQUIRE(picture(pool) == before, "launch %d", good);
+        const bool begun = version != *reinterpret_cast<uint32_t *>(pool.h->base + pool.h->r.version) ||
+                           !std::equal(lengths.begin(), lengths.end(),
+                                       reinterpret_cast<int32_t *>(pool.h->base + pool.h->r.length));
+        std::vector<int32_t> none(c.streams, 0), one(c.streams, 0);
+        one[0] = 1;
+        static uint16_t io[16];
+        void *aligned = reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(io) + 15) & ~uintptr_t(15));
+        if (begun) {                                      // nothing that would read or change the tables
+            REQUIRE(call(pool) == SDV2_E_STATE);
+            REQUIRE(pool.extend(one) == SDV2_E_STATE && pool.attend(one) == SDV2_E_STATE);
+            REQUIRE(pool.free({0}) == (pool.h->tokens[0] > 0 ? SDV2_E_STATE : SDV2_OK));    // (nothing to free)
+            REQUIRE(sdv2_pages_write(pool.h, 0, aligned, aligned, 0, 0, one.data(), nullptr) == SDV2_E_STATE);
+            REQUIRE(pool.compact() == SDV2_E_STATE);
+            REQUIRE(g_launches.empty() && sdv2_pages_check(pool.h) == SDV2_OK && picture(pool) == before);
+        } else {
+            pool.check_books();
+            REQUIRE(call(pool) == SDV2_OK);
+            pool.check_books();
+            REQUIRE(picture(pool) == after);
+        }
+    }
+}
+
+static void failures() {
+    auto grown = [](Pool &p) { REQUIRE(p.extend({100, 0, 37, 0, 0}) == SDV2_OK); };
+    auto forked = [&](Pool &p) {
+        grown(p);
+        REQUIRE(p.fork(0, {1, 3}) == SDV2_OK && p.extend({1, 30, 0, 2, 50}) == SDV2_OK);
+    };
+    auto holes = [&](Pool &p) {
+        forked(p);
+        REQUIRE(p.free({2}) == SDV2_OK);
+    };
+    const sdv2_pages_config small = config(5, 2, 1, 16, 60, 20);
+    every_failure(small, grown, [](Pool &p) { return p.extend({3, 50, 0, 1, 0}); }, 1);
+    every_failure(small, grown, [](Pool &p) { return p.fork(0, {1, 4}); }, 2);
+    every_failure(small, grown, [](Pool &p) { return p.fork(2, {1, 4}, true); }, 2);
+    every_failure(small, forked, [](Pool &p) { return p.free({0, 2}); }, 1);
+    every_failure(small, holes, [](Pool &p) { return p.compact(); }, 2);
+    // more entries and page copies than one launch holds
+    const sdv2_pages_config large = config(5, 2, 1, 16, 12000, 20);
+    auto none = [](Pool &) {};
+    auto many = [](Pool &p) { REQUIRE(p.extend({16 * 2100, 16 * 2500, 0, 0, 5}) == SDV2_OK); };
+    auto gone = [&](Pool &p) {
+        many(p);
+        REQUIRE(p.free({0}) == SDV2_OK);
+    };
+    every_failure(large, none, [](Pool &p) { return p.extend({16 * 2500, 16 * 2000, 0, 0, 5}); }, 3);
+    every_failure(large, many, [](Pool &p) { return p.fork(0, {2, 3}, true); }, 6);
+    every_failure(large, gone, [](Pool &p) { return p.compact(); }, 4);
+}
+
 int main(int argc, char **argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "mixed")
         mixed();
+    else if (what == "failures")
+        failures();
     else if (what == "plan" && argc == 4)
         sessions(std::strtoull(argv[2], nullptr, 10), std::atoi(argv[3]));
     else

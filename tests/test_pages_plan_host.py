@@ -1,5 +1,6 @@
 """The paged cache's host code, compiled for the CPU with the driver and the kernels stood in for
-(host_pages_main.cpp): what the attention's plans cover, no GPU needed."""
+(host_pages_main.cpp): what the attention's plans cover, and that a call which fails leaves the host's books
+and the device's tables alike, no GPU needed."""
 import os
 import shutil
 import subprocess
@@ -36,3 +37,9 @@ def test_plans_of_few_and_many_rows_in_one_call(program):
 def test_plans_of_random_sessions(program, seed):
     """Extends, forks, forks of forks, frees and compactions in any order, any mix of queries."""
     _run(program, "plan", seed, 150)
+
+
+def test_failed_allocations_and_launches(program):
+    """Every allocation and every launch of extend, fork, free and compact failing in turn: the call changes
+    nothing and succeeds when made again; after edits that were launched in part the pool is refused."""
+    _run(program, "failures")
