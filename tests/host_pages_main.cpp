@@ -484,7 +484,7 @@ static void every_failure(const sdv2_pages_config &c, Start start, Call call, in
         REQUIRE(before != after);
     }
     const int every = max(1, allocations / 5);            // (of thousands of like ones a few, and the last ones)
-    for (int i = 0; i <= allocations; i += i + every < allocations - 4 ? every : 1) {
+    for (int i = 0; i <= allocations; i = max(i + 1, min(i + every, allocations - 4))) {
         Pool pool(c);
         start(pool);
         fill_pages(pool);
