@@ -663,6 +663,8 @@ sdv2_status sdv2_cache_create(const sdv2_cache_config *cfg, void *dev_buf, size_
     c->base = static_cast<uint8_t *>(dev_buf);
     cudaError_t e = cudaGetDevice(&c->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device);
+    // (an allocator may have handed the memory out while work of a stream that this one does not wait for is on it)
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemset(dev_buf, 0, g.total);
     if (e != cudaSuccess) {
         delete c;
@@ -1125,6 +1127,8 @@ sdv2_status sdv2_motion_create(const sdv2_motion_config *cfg, void *dev_buf, siz
     }
     h->base = static_cast<uint8_t *>(dev_buf);
     cudaError_t e = cudaGetDevice(&h->device);
+    // (an allocator may have handed the memory out while work of a stream that this one does not wait for is on it)
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemset(dev_buf, 0, h->total);
     std::vector<double> rate(cfg->batch, cfg->s_init);
     if (e == cudaSuccess) e = cudaMemcpy(h->base + h->off_rate, rate.data(), 8ull * cfg->batch, cudaMemcpyHostToDevice);

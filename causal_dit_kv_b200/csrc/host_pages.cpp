@@ -314,6 +314,8 @@ sdv2_status create(const sdv2_pages_config *cfg, void *dev_buf, size_t bytes, sd
     h->group_pages.reserve(c.streams);
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
+    // (an allocator may have handed the memory out while work of a stream that this one does not wait for is on it)
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemset(dev_buf, 0, r.end);
     if (e == cudaSuccess) e = cudaMemset(h->base + r.table, 0xff, 4ull * c.streams * c.stream_pages);
     if (e == cudaSuccess) e = cudaDeviceSynchronize();

@@ -132,9 +132,9 @@ size_t sdv2_cache_bytes(const sdv2_cache_config *cfg);
 sdv2_status sdv2_cache_layout_of(const sdv2_cache_config *cfg, sdv2_cache_layout *out);
 
 /* Bind a cache handle to the caller's device buffer dev_buf of `bytes`
- * bytes (>= sdv2_cache_bytes) on the current device.  Zero-fills the buffer
- * and uploads the RoPE row/column tables, synchronously (not on the hot
- * path).  Every stream starts empty at frame 0.
+ * bytes (>= sdv2_cache_bytes) on the current device.  Waits for the device,
+ * zero-fills the buffer and uploads the RoPE row/column tables, synchronously
+ * (not on the hot path).  Every stream starts empty at frame 0.
  * Limits: head_dim in {64, 128}; batch <= 64; N, H, L, S, W, T' >= 1,
  * W >= T'; sink refresh requires embed_dim >= 1; rope_pairs[0] (temporal
  * pairs) x min(T', floor(255 / N) + 2) <= 128 (the temporal angles of the
@@ -464,7 +464,7 @@ size_t sdv2_pages_bytes(const sdv2_pages_config *cfg);
 sdv2_status sdv2_pages_layout_of(const sdv2_pages_config *cfg, sdv2_pages_layout *out);
 
 /* Bind a handle to the caller's device buffer (256-byte aligned, >= sdv2_pages_bytes) on
- * the current device.  Zero-fills the buffer, synchronously.
+ * the current device.  Waits for the device, then zero-fills the buffer, synchronously.
  *
  * The handle keeps every stream's page list, the tokens of each and the users of each page
  * on the host; the device's tables follow in stream order.  So the calls of one handle belong

@@ -78,16 +78,18 @@ PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() { return encode; }
 }  // namespace sdv2
 
 static int g_sms = 148;
+static bool g_idle = false;                               // nothing that a user's streams do is pending
 
 extern "C" {
 cudaError_t cudaGetDevice(int *d) { return *d = 0, cudaSuccess; }
 cudaError_t cudaDeviceGetAttribute(int *v, cudaDeviceAttr, int) { return *v = g_sms, cudaSuccess; }
 cudaError_t cudaMemset(void *p, int value, size_t n) {
+    REQUIRE(g_idle, "memory is cleared with work pending");
     if (value != 0) std::memset(p, value, n);            // (the buffer is fresh zeros)
     return cudaSuccess;
 }
 cudaError_t cudaMemcpy(void *to, const void *from, size_t n, cudaMemcpyKind) { return std::memcpy(to, from, n), cudaSuccess; }
-cudaError_t cudaDeviceSynchronize() { return cudaSuccess; }
+cudaError_t cudaDeviceSynchronize() { return g_idle = true, cudaSuccess; }
 cudaError_t cudaGetLastError() { return cudaSuccess; }
 const char *cudaGetErrorString(cudaError_t) { return "error"; }
 cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus *s) {
@@ -174,6 +176,7 @@ struct Pool {
         REQUIRE(bytes > 0);
         memory = std::calloc(bytes + 256, 1);
         REQUIRE(memory);
+        g_idle = false;
         void *base = reinterpret_cast<void *>((reinterpret_cast<uintptr_t>(memory) + 255) & ~uintptr_t(255));
         REQUIRE(sdv2_pages_create(&c, base, bytes, &h) == SDV2_OK);
     }
