@@ -92,14 +92,16 @@ class PagedKVCache:
     # -- the path
     def write(self, layer, k, v, counts, stream=None):
         """Keys and values [sum counts, kv_heads, d] of the last counts[b] tokens of each stream."""
-        arr, n = self._counts(counts), sum(counts)
+        arr = self._counts(counts)
+        n = sum(arr)
         kp, ks = self._rows(k, "k", self.kv_heads, n)
         vp, vs = self._rows(v, "v", self.kv_heads, n)
         B.sdv2_pages_write(self.handle, layer, kp or self._any, vp or self._any, ks, vs, arr, stream)
 
     def attention(self, layer, q, out, counts, softmax_scale=None, stream=None):
         """Queries [sum counts, heads, d] of the last counts[b] tokens of each stream over all its keys."""
-        arr, n = self._counts(counts), sum(counts)
+        arr = self._counts(counts)
+        n = sum(arr)
         qp, qs = self._rows(q, "q", self.heads, n)
         op, os_ = self._rows(out, "out", self.heads, n)
         B.sdv2_pages_attention(self.handle, layer, qp or self._any, op or self._any, qs, os_, arr,

@@ -1,5 +1,8 @@
 """What the token-sequence operators' wrappers make of tensors and host numbers before the library is
 called, no GPU needed."""
+from array import array
+
+import numpy as np
 import pytest
 import torch
 
@@ -32,3 +35,29 @@ def test_tokens_that_share_memory_are_refused(x):
     """A token stride of 0 means contiguous to the library, which would read and write past the tensor."""
     with pytest.raises(ValueError, match="overlap"):
         _rows(x)
+
+
+def _pool(monkeypatch, calls):
+    """A PagedKVCache without a device, whose library calls are recorded."""
+    from causal_dit_kv_b200 import PagedKVCache, binding as B
+    for name in ("sdv2_pages_write", "sdv2_pages_attention"):
+        monkeypatch.setattr(B, name, lambda *args: calls.append(args))
+    c = PagedKVCache.__new__(PagedKVCache)
+    c.handle, c.device, c.dtype, c._any, c._scale = None, -1, torch.bfloat16, 16, 0.125
+    c.streams, c.heads, c.kv_heads, c.head_dim = 2, H, H, D
+    return c
+
+
+@pytest.mark.parametrize("make", [
+    list, tuple, lambda x: np.array(x, np.int8), lambda x: np.array(x, np.int64), torch.tensor,
+    lambda x: torch.tensor(x, dtype=torch.int8), lambda x: array("b", x)])
+def test_counts_of_any_width_add_up(monkeypatch, make):
+    """Counts whose sum does not fit their own type."""
+    calls = []
+    c = _pool(monkeypatch, calls)
+    x = torch.zeros((200, H, D), dtype=torch.bfloat16)
+    c.write(0, x, x, make([100, 100]))
+    c.attention(0, x, x.clone(), make([100, 100]))
+    assert list(calls[0][6]) == [100, 100] and list(calls[1][6]) == [100, 100]
+    with pytest.raises(ValueError, match="199 tokens"):
+        c.write(0, x[:199], x, make([100, 100]))
