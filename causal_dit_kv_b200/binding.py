@@ -12,6 +12,7 @@ import ctypes
 import os
 from array import array
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_uint64, c_void_p
+from operator import index
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsdv2.so")
 
@@ -384,15 +385,24 @@ def sdv2_prompt_check() -> int:
     return int(lib().sdv2_prompt_check())
 
 
+def _int32(value) -> int:
+    """A host integer that the library takes in 32 bits (ctypes alone would take it modulo 2^32)."""
+    value = index(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise OverflowError(f"{value} does not fit 32 bits")
+    return value
+
+
 def make_pages_config(streams, layers, heads, kv_heads, head_dim, pages, page_tokens=64, stream_pages=None,
                       max_queries=None, block_tokens=1, dtype="bf16") -> sdv2_pages_config:
     """stream_pages None: as many as the pool has (within the limit); max_queries None: one for every stream."""
     cfg = sdv2_pages_config()
-    cfg.streams, cfg.layers, cfg.heads, cfg.kv_heads, cfg.head_dim = streams, layers, heads, kv_heads, head_dim
-    cfg.page_tokens, cfg.pages = page_tokens, pages
-    cfg.stream_pages = min(pages, (1 << 25) // max(page_tokens, 1)) if stream_pages is None else stream_pages
-    cfg.max_queries = streams if max_queries is None else max_queries
-    cfg.block_tokens = min(block_tokens, (1 << 31) - 1)
+    stream_pages = min(pages, (1 << 25) // max(page_tokens, 1)) if stream_pages is None else stream_pages
+    for name, value in (("streams", streams), ("layers", layers), ("heads", heads), ("kv_heads", kv_heads),
+                        ("head_dim", head_dim), ("page_tokens", page_tokens), ("pages", pages),
+                        ("stream_pages", stream_pages), ("max_queries", streams if max_queries is None else max_queries),
+                        ("block_tokens", min(block_tokens, (1 << 31) - 1))):
+        setattr(cfg, name, _int32(value))
     cfg.dtype = DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
     return cfg
 
@@ -437,20 +447,20 @@ def sdv2_pages_extend(pages: int, counts, stream=None) -> None:
 
 def sdv2_pages_write(pages: int, layer: int, k, v, k_stride: int, v_stride: int, counts, stream=None) -> None:
     arr = int32_array(counts)
-    _check(lib().sdv2_pages_write(pages, layer, _ptr(k), _ptr(v), k_stride, v_stride, _address(arr), _stream(stream)),
+    _check(lib().sdv2_pages_write(pages, _int32(layer), _ptr(k), _ptr(v), k_stride, v_stride, _address(arr), _stream(stream)),
            "sdv2_pages_write")
 
 
 def sdv2_pages_attention(pages: int, layer: int, q, out, q_stride: int, out_stride: int, counts, softmax_scale: float,
                          stream=None) -> None:
     arr = int32_array(counts)
-    _check(lib().sdv2_pages_attention(pages, layer, _ptr(q), _ptr(out), q_stride, out_stride, _address(arr),
+    _check(lib().sdv2_pages_attention(pages, _int32(layer), _ptr(q), _ptr(out), q_stride, out_stride, _address(arr),
                                       softmax_scale, _stream(stream)), "sdv2_pages_attention")
 
 
 def sdv2_pages_fork(pages: int, src: int, dst, deep: bool = False, stream=None) -> None:
     arr = int32_array(dst)
-    _check(lib().sdv2_pages_fork(pages, src, _address(arr), len(arr), 1 if deep else 0, _stream(stream)),
+    _check(lib().sdv2_pages_fork(pages, _int32(src), _address(arr), len(arr), 1 if deep else 0, _stream(stream)),
            "sdv2_pages_fork")
 
 
@@ -467,6 +477,7 @@ def sdv2_pages_compact(pages: int, stream=None) -> int:
 
 def sdv2_pages_query(pages: int, stream_index: int):
     """(tokens, list of page ids, leading pages shared by the stream's whole group)."""
+    stream_index = _int32(stream_index)
     tokens, n, shared = c_int32(), c_int32(), c_int32()
     _check(lib().sdv2_pages_query(pages, stream_index, ctypes.byref(tokens), None, 0, ctypes.byref(n),
                                   ctypes.byref(shared)), "sdv2_pages_query")
@@ -479,7 +490,7 @@ SHARE_MODES = {"never": 0, "auto": 1, "always": 2}
 
 
 def sdv2_pages_share(pages: int, mode) -> None:
-    _check(lib().sdv2_pages_share(pages, SHARE_MODES[mode] if isinstance(mode, str) else int(mode)), "sdv2_pages_share")
+    _check(lib().sdv2_pages_share(pages, SHARE_MODES[mode] if isinstance(mode, str) else _int32(mode)), "sdv2_pages_share")
 
 
 def sdv2_pages_used(pages: int) -> int:

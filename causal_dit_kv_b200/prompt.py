@@ -60,7 +60,7 @@ def prompt_attention(q, k, v, out, offsets, block_tokens=1, softmax_scale=None, 
         if any(int(x) != 0 for x in offsets):
             raise ValueError("offsets must lie in 0..tokens")
         return
-    cfg = B.sdv2_prompt_config(heads, kv_heads, d, min(block_tokens, (1 << 31) - 1), _DTYPE[dtype], tokens, qs, ks, vs, os_)
+    cfg = B.sdv2_prompt_config(heads, kv_heads, d, B._int32(min(block_tokens, (1 << 31) - 1)), _DTYPE[dtype], tokens, qs, ks, vs, os_)
     B.sdv2_prompt_attention(cfg, qp, kp, vp, op, offsets, 1.0 / math.sqrt(d) if softmax_scale is None else softmax_scale,
                             stream)
 

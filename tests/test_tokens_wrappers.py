@@ -61,3 +61,28 @@ def test_counts_of_any_width_add_up(monkeypatch, make):
     assert list(calls[0][6]) == [100, 100] and list(calls[1][6]) == [100, 100]
     with pytest.raises(ValueError, match="199 tokens"):
         c.write(0, x[:199], x, make([100, 100]))
+
+
+@pytest.mark.parametrize("name", ["streams", "layers", "heads", "kv_heads", "head_dim", "pages", "page_tokens",
+                                  "stream_pages", "max_queries"])
+def test_numbers_past_32_bits_are_refused(name):
+    """Not taken modulo 2^32."""
+    from causal_dit_kv_b200 import binding as B
+    good = dict(streams=4, layers=2, heads=8, kv_heads=2, head_dim=64, pages=100, page_tokens=64, stream_pages=50,
+                max_queries=16)
+    assert B.sdv2_pages_bytes(B.make_pages_config(**good)) > 0
+    with pytest.raises(OverflowError):
+        B.make_pages_config(**{**good, name: good[name] + (1 << 32)})
+    with pytest.raises(OverflowError):
+        B.make_pages_config(**good, block_tokens=1 - (1 << 32))
+    assert B.make_pages_config(**good, block_tokens=1 << 40).block_tokens == (1 << 31) - 1
+
+
+def test_arguments_past_32_bits_are_refused():
+    from causal_dit_kv_b200 import binding as B
+    for call in (lambda: B.sdv2_pages_write(None, 1 << 32, 16, 16, 0, 0, [1], 0),
+                 lambda: B.sdv2_pages_attention(None, 1 << 32, 16, 16, 0, 0, [1], 1.0, 0),
+                 lambda: B.sdv2_pages_fork(None, 1 << 32, [1], False, 0), lambda: B.sdv2_pages_share(None, 1 << 32),
+                 lambda: B.sdv2_pages_query(None, 1 << 32)):
+        with pytest.raises(OverflowError):
+            call()
