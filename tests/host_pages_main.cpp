@@ -4,6 +4,7 @@
 //
 //   host_pages_main plan SEED N     plans of N random sessions cover every query's keys exactly once
 //   host_pages_main mixed           plans of calls that mix few and many query rows
+//   host_pages_main share           which groups read their common pages once
 //   host_pages_main failures        calls that change the tables, with every allocation and launch failing in turn
 #include <cstdarg>
 #include <cstdio>
@@ -384,6 +385,43 @@ static void mixed() {
                 }
 }
 
+// ---------------------------------------------------------------- the sharing rule
+// Whether `members` streams with `each` queries read their `pages` common pages of 16 KB (a layer's keys
+// and values) once.  `idle` more members have no queries.
+static bool shares(int mode, int32_t members, int32_t each, int32_t pages, int32_t idle = 0) {
+    const int32_t n = members + idle;
+    Pool pool(config(n, 4, 4, 16, pages + n * (each / 16 + 2), n * each));
+    REQUIRE(sdv2_pages_share(pool.h, mode) == SDV2_OK);
+    std::vector<int32_t> first(n, 0), counts(n, each), others;
+    first[0] = pages * 16;
+    for (int32_t b = 1; b < n; ++b) others.push_back(b);
+    REQUIRE(pool.extend(first) == SDV2_OK && pool.fork(0, others) == SDV2_OK && pool.extend(counts) == SDV2_OK);
+    std::fill(counts.begin() + members, counts.end(), 0);
+    REQUIRE(pool.attend(counts) == SDV2_OK);
+    REQUIRE(g_is_small && g_small.n_common <= 1);
+    check_plan(pool, counts);
+    if (g_small.n_common == 1) REQUIRE(g_small.section[0].keys == pages * 16);
+    return g_small.n_common == 1;
+}
+
+static void share() {
+    const int never = SDV2_SHARE_NEVER, automatic = SDV2_SHARE_AUTO, always = SDV2_SHARE_ALWAYS;
+    REQUIRE(shares(always, 2, 1, 1) && shares(always, 2, 40, 1) && !shares(always, 1, 1, 5000, 3));
+    REQUIRE(!shares(never, 8, 1, 5000) && !shares(never, 8, 40, 5000));
+    // at most 16 rows: from five members on, where 24 MB are read less
+    REQUIRE(shares(automatic, 5, 1, 384) && !shares(automatic, 5, 1, 383));
+    REQUIRE(shares(automatic, 5, 3, 384) && !shares(automatic, 5, 3, 383));
+    REQUIRE(shares(automatic, 16, 1, 103) && !shares(automatic, 16, 1, 102));
+    REQUIRE(shares(automatic, 5, 1, 384, 7) && !shares(automatic, 5, 1, 383, 7));       // (idle members save nothing)
+    // more rows: where 30 MB and 4 for every member are
+    REQUIRE(shares(automatic, 5, 4, 800) && !shares(automatic, 5, 4, 799));
+    REQUIRE(shares(automatic, 17, 1, 392) && !shares(automatic, 17, 1, 391));
+    REQUIRE(shares(automatic, 2, 9, 2432) && !shares(automatic, 2, 9, 2431));
+    // over 64 MB in any case
+    REQUIRE(shares(automatic, 4, 1, 4097) && !shares(automatic, 4, 1, 4096));
+    REQUIRE(shares(automatic, 2, 8, 4097) && !shares(automatic, 2, 8, 4096));
+}
+
 // ---------------------------------------------------------------- random sessions
 static void sessions(uint64_t seed, int n) {
     std::mt19937_64 rng(seed);
@@ -569,6 +607,8 @@ int main(int argc, char **argv) {
     const std::string what = argc > 1 ? argv[1] : "";
     if (what == "mixed")
         mixed();
+    else if (what == "share")
+        share();
     else if (what == "failures")
         failures();
     else if (what == "plan" && argc == 4)

@@ -39,6 +39,11 @@ def test_plans_of_random_sessions(program, seed):
     _run(program, "plan", seed, 150)
 
 
+def test_the_sharing_rule_on_both_sides_of_its_borders(program):
+    """Automatic, always and never; up to 16 rows to a key head and more; idle members."""
+    _run(program, "share")
+
+
 def test_failed_allocations_and_launches(program):
     """Every allocation and every launch of extend, fork, free and compact failing in turn: the call changes
     nothing and succeeds when made again; after edits that were launched in part the pool is refused."""
