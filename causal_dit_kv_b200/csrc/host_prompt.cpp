@@ -53,8 +53,7 @@ void order_items(const int32_t *len, int n_seqs, int rows, int64_t block, std::v
 template <int kItems>
 sdv2_status launch_items(const sdv2_prompt_config &c, void *out, int64_t out_stride, float scale, const int32_t *first,
                          const int32_t *len, int n_seqs, const uint32_t *items, int n_items, bool pair,
-                         const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, int sm_count,
-                         cudaStream_t s) {
+                         const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t s) {
     // (every field and entry that the kernel reads is set below)
     std::unique_ptr<PromptParams<kItems>> p(new PromptParams<kItems>);
     p->out = static_cast<uint16_t *>(out);
@@ -77,7 +76,7 @@ sdv2_status launch_items(const sdv2_prompt_config &c, void *out, int64_t out_str
     std::copy(first, first + n_seqs, p->seq_first);
     std::copy(len, len + n_seqs, p->seq_len);
     std::copy(items, items + n_items, p->item);
-    cudaError_t e = launch_prompt<kItems>(*p, tq, tk, tv, c.head_dim, c.dtype == SDV2_DT_FP16, sm_count, s);
+    cudaError_t e = launch_prompt<kItems>(*p, tq, tk, tv, c.head_dim, c.dtype == SDV2_DT_FP16, s);
     if (e != cudaSuccess) return cuda_fail(e, "prompt_attention launch");
     count_launch();
     return SDV2_OK;
@@ -119,10 +118,6 @@ sdv2_status prompt_attention(const sdv2_prompt_config *cfg, const void *q, const
     c.block_tokens = static_cast<int32_t>(std::min<int64_t>(c.block_tokens, c.tokens));
 
     if (!get_encode_fn()) return fail(SDV2_E_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return cuda_fail(e, "prompt_attention");
     const bool half = c.dtype == SDV2_DT_FP16;
     CUtensorMap tq, tk, tv;
     if (!map_tokens(&tq, q, half, c.head_dim, c.heads, c.tokens, c.q_stride) ||
@@ -147,9 +142,9 @@ sdv2_status prompt_attention(const sdv2_prompt_config *cfg, const void *q, const
             const sdv2_status st =
                 m <= kPromptSmallItems
                     ? launch_items<kPromptSmallItems>(c, out, c.out_stride, scale, first, len, n, items.data() + i, m,
-                                                      pair, tq, tk, tv, sms, s)
+                                                      pair, tq, tk, tv, s)
                     : launch_items<kPromptLargeItems>(c, out, c.out_stride, scale, first, len, n, items.data() + i, m,
-                                                      pair, tq, tk, tv, sms, s);
+                                                      pair, tq, tk, tv, s);
             if (st != SDV2_OK) return st;
         }
     }

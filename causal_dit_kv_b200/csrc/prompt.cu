@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 template <int D, bool HALF, int kItems>
 static cudaError_t launch_prompt_d(const PromptParams<kItems> &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                                   const CUtensorMap &tv, int sm_count, cudaStream_t s) {
+                                   const CUtensorMap &tv, cudaStream_t s) {
     // (an attribute of the current device's copy of the kernel: set once per device)
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
@@ -470,27 +470,24 @@ static cudaError_t launch_prompt_d(const PromptParams<kItems> &p, const CUtensor
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    (void)sm_count;
     return launch_dependent(prompt_attention_kernel<D, HALF, kItems>, dim3(p.n_units), dim3(kAttnThreads),
                             static_cast<size_t>(PromptLayout<D>::kAlloc), s, p, tq, tk, tv);
 }
 
 template <int kItems>
 cudaError_t launch_prompt(const PromptParams<kItems> &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                          const CUtensorMap &tv, int head_dim, bool half, int sm_count, cudaStream_t s) {
+                          const CUtensorMap &tv, int head_dim, bool half, cudaStream_t s) {
     if (head_dim == 64)
-        return half ? launch_prompt_d<64, true>(p, tq, tk, tv, sm_count, s)
-                    : launch_prompt_d<64, false>(p, tq, tk, tv, sm_count, s);
-    return half ? launch_prompt_d<128, true>(p, tq, tk, tv, sm_count, s)
-                : launch_prompt_d<128, false>(p, tq, tk, tv, sm_count, s);
+        return half ? launch_prompt_d<64, true>(p, tq, tk, tv, s)
+                    : launch_prompt_d<64, false>(p, tq, tk, tv, s);
+    return half ? launch_prompt_d<128, true>(p, tq, tk, tv, s)
+                : launch_prompt_d<128, false>(p, tq, tk, tv, s);
 }
 
 template cudaError_t launch_prompt<kPromptSmallItems>(const PromptParams<kPromptSmallItems> &, const CUtensorMap &,
-                                                      const CUtensorMap &, const CUtensorMap &, int, bool, int,
-                                                      cudaStream_t);
+                                                      const CUtensorMap &, const CUtensorMap &, int, bool, cudaStream_t);
 template cudaError_t launch_prompt<kPromptLargeItems>(const PromptParams<kPromptLargeItems> &, const CUtensorMap &,
-                                                      const CUtensorMap &, const CUtensorMap &, int, bool, int,
-                                                      cudaStream_t);
+                                                      const CUtensorMap &, const CUtensorMap &, int, bool, cudaStream_t);
 
 cudaError_t prompt_status(uint32_t *word) {
     cudaError_t e = cudaMemcpyFromSymbol(word, g_prompt_status, sizeof(uint32_t));

@@ -28,7 +28,7 @@ struct PromptParams {
 
 template <int kItems>
 cudaError_t launch_prompt(const PromptParams<kItems> &p, const CUtensorMap &tq, const CUtensorMap &tk,
-                          const CUtensorMap &tv, int head_dim, bool half, int sm_count, cudaStream_t s);
+                          const CUtensorMap &tv, int head_dim, bool half, cudaStream_t s);
 // Reads and clears the device word in which the prompt kernels record waits that ran out.
 cudaError_t prompt_status(uint32_t *word);
 
