@@ -1,5 +1,7 @@
 """Paged attention calls whose streams bring different numbers of queries (B200): viewers on their
 next token, in a group that reads its common pages once, beside streams of many queries."""
+import random
+
 import pytest
 import torch
 
@@ -55,3 +57,50 @@ def test_a_replay_of_a_mixed_call(mode):
         q.copy_(m.normal(n, 8, 128))
         graph.replay()
         m.attend(0, counts, q=q, run=lambda layer, q, o, c, s: o.copy_(out))
+
+
+def test_the_same_bits_again():
+    """Calls of every combination of kernels repeat themselves exactly."""
+    m, counts = _session("always", (8, 8), 128, "bf16", 5000, 40)
+    for call in (counts, [1] * 8 + [0, 1], [3, 1, 1, 1, 4, 6, 1, 1, 0, 2], [0] * 8 + [0, 40]):
+        q = m.normal(sum(call), 8, 128)
+        first = m.attend(0, call, q=q)
+        for _ in range(5):
+            again = torch.empty_like(q)
+            m.c.attention(0, q, again, call)
+            assert torch.equal(first, again)
+
+
+@pytest.mark.parametrize("seed", range(10))
+def test_random_sessions(seed):
+    """Extends, forks, forks of forks, frees and compactions in any order, any mix of queries."""
+    r = random.Random(seed)
+    heads, kv_heads = r.choice([(4, 2), (10, 2), (8, 1), (12, 12), (6, 3)])
+    streams, page = r.randint(3, 10), r.choice([16, 32, 64, 128])
+    m = Model(seed=seed, share=r.choice(["auto", "always", "never"]),
+              **cfg(streams=streams, heads=heads, kv_heads=kv_heads, head_dim=r.choice([64, 128]), page_tokens=page,
+                    dtype=r.choice(["bf16", "fp16"]), pages=12000 // page, max_queries=2000, layers=r.randint(1, 2),
+                    block_tokens=r.choice([1, 1, 7, 64])))
+    for _ in range(14):
+        what = r.choice(["grow", "grow", "grow", "fork", "fork", "free", "compact"])
+        if what == "grow":
+            counts = [r.choice([0, 1, r.randint(1, 3 * page), r.randint(1, 900)]) for _ in range(streams)]
+            need = sum(-(-(m.tokens(b) + x) // page) - len(m.lists[b]) for b, x in enumerate(counts))
+            if need <= m.users.count(0):
+                m.grow(counts)
+        elif what == "fork":
+            src = r.randrange(streams)
+            dst = [b for b in range(streams) if b != src and m.tokens(b) == 0 and r.random() < 0.7]
+            deep = r.random() < 0.15
+            copied = len(m.lists[src]) - (0 if deep else m.tokens(src) // page)
+            if m.tokens(src) and copied * len(dst) <= m.users.count(0):
+                m.fork(src, dst, deep)
+        elif what == "free":
+            m.free([r.randrange(streams)])
+        else:
+            m.compact()
+        m.check()
+        most = r.choice([1, 3, 20, 200])
+        counts = [min(m.tokens(b), r.choice([0, 1, 1, r.randint(1, most)])) for b in range(streams)]
+        if sum(counts):
+            m.attend(r.randrange(m.kw["layers"]), counts)
