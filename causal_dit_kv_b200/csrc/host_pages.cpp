@@ -430,6 +430,8 @@ sdv2_status write(sdv2_pages *h, int32_t layer, const void *k, const void *v, in
 // 2048 47 / 33, 8192 138 / 45; 16 streams: 1024 15 / 17, 2048 18 / 17, 8192 41 / 25; 4 streams of
 // 12 heads x 64, 16 tokens each: 2048 16 / 16, 8192 24 / 26.  16 rows or fewer: 16 streams of 12
 // heads x 128: 256 11.7 / 11.1, 8192 58 / 20; 4 streams of 32/8: 8192 17.5 / 19.
+// (Beside a stream of many rows the tile kernel takes these too: 16 streams of 12 heads x 128 beside 64
+// queries of another, 4096 common keys 64 / 26, 8192 114 / 28.)
 bool shared(const sdv2_pages *h, int64_t members, int64_t pages, int64_t rows) {
     if (h->share != SDV2_SHARE_AUTO) return h->share == SDV2_SHARE_ALWAYS;
     const int64_t mb = 1 << 20;
@@ -538,6 +540,8 @@ sdv2_status attend(sdv2_pages *h, int32_t layer, const void *q, void *out, int64
 
     // Both parts' kernels: a warp per run where no unit has more than 16 rows.  A stream outside every
     // group may have more rows than the groups: one launch of the tile kernel takes both parts then.
+    // (16 forks' next tokens on 8192 common keys beside 64 queries of another stream, 12 heads x 128: 27.9 us;
+    // as two calls, each with its own kernel, 19.3 and 15.2.  40/8 heads: 28.3; 22.4 and 16.3.)
     const int32_t own_rows = most_tokens * p->group, common_rows = most_common * p->group;
     const bool few_own = own_rows <= kRowsPerWorker, few_common = few_own && common_rows <= kRowsPerWorker;
     auto work = [&](int begin, int end, bool few, int32_t rows, int32_t cut_row) {

@@ -12,8 +12,8 @@
 //
 // Writes: one warp per new token; it looks up the token's stream, page and place once
 // and moves the token's keys and values, 16 bytes a lane.  Bound by HBM: 8192 tokens of 40 heads
-// of 128 (336 MB moved) 56 us, 6.0 TB/s; for a step's few tokens by the call: 64 tokens of 8
-// heads 8.7 us.
+// of 128 (336 MB moved) 56 to 57 us, 5.9 TB/s; for a step's few tokens by the call: 64 tokens of 8
+// heads 8.7 to 9.2 us.
 #include "ptx.cuh"
 #include "token_ops.h"
 

@@ -24,8 +24,8 @@
 // What bounds it with full tiles: the chain of a tile (scores, softmax, product) on two sets, and
 // a run's start and end (about five tiles' time, counted when the work is cut).  16 streams of 64
 // queries on 4000 common keys and up to 900 of their own, 12 heads of 64, fp16: 52.3 us, 35 MB read,
-// tensor pipe 27 %; 64 streams of one query on 16384 common keys, 40/8 heads of 128: 62 us with
-// the row kernel's part and the merge.
+// tensor pipe 27 %; 64 streams of one query on 16384 common keys, 40/8 heads of 128: 62 to 64 us
+// with the row kernel's part and the merge.
 #include <atomic>
 
 #include "attn_core.cuh"

@@ -21,8 +21,8 @@
 // them sees a score over it by more than 2^8, so an ordinary tile has one vote and no reduction.
 // Keys past the range are copied as zeros and their scores masked.
 //
-// 32 streams of 500 to 8000 keys, 32/8 heads of 128, bf16: 604 MB in 97 us with the merge, 6.2 TB/s;
-// one stream of 1000 keys, 12 heads: 7.6 us, of which two launches and a run's chain of copies are
+// 32 streams of 500 to 8000 keys, 32/8 heads of 128, bf16: 604 MB in 97 to 98.5 us with the merge, 6.1 TB/s;
+// one stream of 1000 keys, 12 heads: 7.6 to 8.0 us, of which two launches and a run's chain of copies are
 // nearly all.
 #include <algorithm>
 #include <atomic>

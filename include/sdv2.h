@@ -435,7 +435,8 @@ typedef struct {
     int32_t page_tokens;    /* n: tokens of a page: 16, 32, 64 or 128 */
     int32_t pages;          /* P: pages of the pool (a page holds its tokens in every layer) */
     int32_t stream_pages;   /* pages that one stream can have, at most; x page_tokens <= 2^25 */
-    int32_t max_queries;    /* query tokens of one attention call, all streams together */
+    int32_t max_queries;    /* query tokens of one attention call, all streams together; the
+                             * scratch holds 2 x max_queries x Hq rows of d + 2 fp32 values */
     int32_t block_tokens;   /* b >= 1: attention is causal by blocks of b tokens (1: token by token) */
     int32_t dtype;          /* SDV2_DT_BF16 or SDV2_DT_FP16 */
 } sdv2_pages_config;
@@ -509,7 +510,7 @@ sdv2_status sdv2_pages_write(sdv2_pages *pages, int32_t layer, const void *k, co
  *   the stream takes no part), their sum at most max_queries.  out overlaps no input.
  * Streams that share their leading pages (sdv2_pages_fork) have those read and multiplied
  * once for all of them, where that is faster (sdv2_pages_share): one group per first page,
- * over the pages that all its streams have in common.  Roundings as in
+ * over the pages that all its streams have in common, those without queries included.  Roundings as in
  * sdv2_prompt_attention; what a page holds behind its stream's last token has no part in
  * the result; a value that is not finite in a stream's tokens may reach any of its queries.
  * Errors: SDV2_E_ARG, SDV2_E_SHAPE, SDV2_E_ALIGN; SDV2_E_STATE if a stream has fewer
